@@ -25,6 +25,9 @@
  * "Quantization: BF16 vs NVFP4": moe_nvfp4_*); and expert parallelism with the
  * exchange done by the dispatch and combine kernels through peer pointers
  * (§02d's all-to-all schedule: moe_ep_*, with CUDA IPC mappings moe_ipc_*).
+ * Two serving forms of the same layer have no counterpart on the pages: experts
+ * in 8-bit integers with a scale per token and per output channel (moe_int8_*),
+ * and the whole layer for a few tokens in one kernel (moe_few_tokens*).
  *
  * Conventions for every call
  * --------------------------
@@ -43,7 +46,8 @@
  *  - T = 0 (no tokens) is valid: the call does nothing except what it states
  *    (moe_router_topk still zeroes counts).
  *  - Host-only calls (no stream, nothing launched): moe_permute_scratch_bytes,
- *    moe_nvfp4_rows_capacity, moe_capacity_for, moe_status_string,
+ *    moe_nvfp4_rows_capacity, moe_few_tokens_scratch_bytes, moe_capacity_for,
+ *    moe_status_string,
  *    moe_set_wait_timeout_ns and the moe_ipc_* mappings.
  */
 #ifndef MOE_H
@@ -84,6 +88,8 @@ typedef uint16_t moe_bf16;
 #define MOE_MAX_SHARED 8
 #define MOE_MAX_GROUPS 1024
 #define MOE_EP_MAX_WORLD 64 /* ranks of an expert-parallel group */
+#define MOE_FEW_MAX_T 64    /* tokens of a moe_few_tokens call */
+#define MOE_FEW_MAX_WIDTH 32768 /* its largest d and d_ff */
 
 /*
  * moe_router_topk -- router scores, biased top-k, joint gates, load counts.
@@ -368,6 +374,97 @@ int moe_nvfp4_grouped_gemm(const uint8_t* aq, const uint8_t* asf, const int32_t*
  */
 int moe_combine(const moe_bf16* y_perm, const int32_t* token_row, const float* gates, const moe_bf16* y_shared,
                 int T, int d, int top_k, int n_shared, moe_bf16* out, void* stream);
+
+/*
+ * 8-bit experts (W8A8): weights and activations in signed 8-bit codes, one fp32
+ * scale per weight row (output channel) and per activation row (token).
+ * A row v of K values: a = max |v|, scale = fl32(a / 127), code = 127 v / a rounded
+ * to the nearest integer, ties to even (the exact code of the bf16 values; -127 ..
+ * 127).  A row of zeros has scale 0 and codes 0; a row that holds a NaN or an
+ * infinity has scale NaN and codes 0, so everything computed from it is NaN.
+ */
+
+/*
+ * moe_int8_quantize_rows -- codes and scales of rows, one scale a row.  For
+ * weights, rows = all matrices' rows (e.g. (n_routed + n_shared) * d_ff).
+ *   x      [rows, K] bf16
+ *   q      [rows, K] int8 out; scale [rows] fp32 out
+ * Limits: K % 8 == 0.
+ */
+int moe_int8_quantize_rows(const moe_bf16* x, long long rows, int K, int8_t* q, float* scale, void* stream);
+
+/*
+ * moe_int8_dispatch -- the 8-bit dispatch: each token's x row is coded once and
+ * written to the rows of its routed experts.
+ *   x          [T, d] bf16; token_row [T, top_k] from moe_permute (or
+ *              moe_permute_capped: entries outside [0, n_rows), such as -1, are skipped)
+ *   xq, xs     [n_rows, d] int8 and [n_rows] fp32 out: the routed experts' rows;
+ *              rows no entry names are left as they were
+ *   xq_tok, xs_tok  [T, d] int8 and [T] fp32 out: the same in token order, for the
+ *              shared experts; both NULL when not wanted
+ * Limits: d % 8 == 0, 1 <= top_k <= 8.
+ */
+int moe_int8_dispatch(const moe_bf16* x, const int32_t* token_row, int T, int d, int top_k, int n_rows, int8_t* xq,
+                      float* xs, int8_t* xq_tok, float* xs_tok, void* stream);
+
+#define MOE_INT8_EPI_BF16 0   /* out = bf16(u) */
+#define MOE_INT8_EPI_GELU 1   /* out = bf16(gelu(u)) */
+#define MOE_INT8_EPI_SWIGLU 2 /* weights [*, 2N, K] (gate rows, then up rows): out = bf16(silu(u_gate) * u_up) */
+
+/*
+ * moe_int8_grouped_gemm -- 8-bit products for groups of rows (tcgen05.mma
+ * kind::i8, exact int32 sums): u[r, n] = (a_scale[r] * w_scale[e, n]) *
+ * sum_k aq[r, k] * wq[e, n, k], then the epilogue.
+ *   aq         [n_rows, K] int8, a_scale [n_rows] fp32
+ *   offsets    [n_groups + 1] int32 (device; values are clamped to [0, n_rows]) or
+ *              NULL.  Non-NULL: group g is rows offsets[g] .. offsets[g+1]-1 and
+ *              out is [n_rows, N]; rows of no group are left as they were.  NULL:
+ *              every group sees all n_rows rows and out is [n_groups, n_rows, N].
+ *   expert_base  group g uses expert e = expert_base + g
+ *   wq         [*, N, K] int8 all experts' matrices ([*, 2N, K] for SWIGLU);
+ *              w_scale [*, N] (or [*, 2N]) fp32
+ * Limits: K % 16 == 0, K <= 131072 (the sums fit 32 bits), N % 32 == 0,
+ * n_groups <= MOE_MAX_GROUPS.
+ */
+int moe_int8_grouped_gemm(const int8_t* aq, const float* a_scale, const int32_t* offsets, int n_groups, int n_rows,
+                          int expert_base, const int8_t* wq, const float* w_scale, int N, int K, int epilogue,
+                          moe_bf16* out, void* stream);
+
+/*
+ * moe_few_tokens, moe_few_tokens_int8 -- the whole layer for at most
+ * MOE_FEW_MAX_T tokens (decoding) in one kernel: moe_router_topk, the experts and
+ * moe_combine with nothing between them.  Arguments and results as of those calls:
+ *   x, w_router, bias, logit_offset, route_scale, topk_idx, gates, counts as
+ *   moe_router_topk (counts is written whole, ready for moe_bias_update; a score
+ *   that is NaN is chosen last); w1, w2, activation as moe_experts_ffn;
+ *   out        [T, d] bf16: the layer's output
+ * bf16 experts: fp32 sums; the hidden rows keep 16 significant bits and the
+ * experts' outputs are added in fp32 (moe_experts_ffn and moe_combine round both
+ * to bf16 on the way).
+ * 8-bit experts: w1 [n, d_ff, d] (SwiGLU [n, 2*d_ff, d]) and w2 [n, d, d_ff] int8
+ * with scales w1_scale [n, d_ff or 2*d_ff] and w2_scale [n, d] from
+ * moe_int8_quantize_rows, n = n_routed + n_shared; x rows and hidden rows (the
+ * fp32 values) are coded as moe_int8_quantize_rows does.
+ *   scratch    device buffer of at least moe_few_tokens_scratch_bytes(...) bytes,
+ *              16-byte aligned, contents need not be initialised; calls that share
+ *              one must be ordered
+ * Results do not depend on timing: equal inputs give equal bits.
+ * The launch is cooperative (one CTA per SM, all resident); its internal waits are
+ * bounded by moe_set_wait_timeout_ns.
+ * Limits: T <= MOE_FEW_MAX_T, d % 64 == 0, d_ff % 64 == 0, d and d_ff <=
+ * MOE_FEW_MAX_WIDTH, n_routed <= 256, n_shared <= 8, top_k <= 8.
+ * MOE_ERR_SCRATCH when scratch_bytes is too small.
+ */
+size_t moe_few_tokens_scratch_bytes(int T, int d, int d_ff, int n_routed, int n_shared, int top_k);
+int moe_few_tokens(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const float* logit_offset,
+                   const moe_bf16* w1, const moe_bf16* w2, int T, int d, int d_ff, int n_routed, int n_shared,
+                   int top_k, float route_scale, int activation, int32_t* topk_idx, float* gates, int32_t* counts,
+                   moe_bf16* out, void* scratch, size_t scratch_bytes, void* stream);
+int moe_few_tokens_int8(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const float* logit_offset,
+                        const int8_t* w1, const float* w1_scale, const int8_t* w2, const float* w2_scale, int T,
+                        int d, int d_ff, int n_routed, int n_shared, int top_k, float route_scale, int activation,
+                        int32_t* topk_idx, float* gates, int32_t* counts, moe_bf16* out, void* scratch,
+                        size_t scratch_bytes, void* stream);
 
 /*
  * moe_bias_update -- the aux-loss-free balancing controller, in place.

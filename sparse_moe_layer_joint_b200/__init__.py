@@ -43,6 +43,10 @@ MOE_ACT_SWIGLU = 1
 MOE_NVFP4_EPI_GELU_FP4 = 0
 MOE_NVFP4_EPI_BF16 = 1
 MOE_NVFP4_EPI_SWIGLU_FP4 = 2
+MOE_INT8_EPI_BF16 = 0
+MOE_INT8_EPI_GELU = 1
+MOE_INT8_EPI_SWIGLU = 2
+MOE_FEW_MAX_T = 64
 
 _vp, _i32, _u64, _f32, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64, ctypes.c_float, ctypes.c_size_t
 
@@ -67,6 +71,15 @@ _lib.moe_nvfp4_rows_capacity.restype = _i64
 _lib.moe_nvfp4_dispatch.argtypes = [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]
 _lib.moe_nvfp4_grouped_gemm.argtypes = [_vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
                                         _vp, _i64, _vp]
+_lib.moe_int8_quantize_rows.argtypes = [_vp, _i64, _i32, _vp, _vp, _vp]
+_lib.moe_int8_dispatch.argtypes = [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]
+_lib.moe_int8_grouped_gemm.argtypes = [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp]
+_lib.moe_few_tokens_scratch_bytes.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32]
+_lib.moe_few_tokens_scratch_bytes.restype = _sz
+_lib.moe_few_tokens.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _vp,
+                                _vp, _vp, _vp, _sz, _vp]
+_lib.moe_few_tokens_int8.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
+                                     _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
 _lib.moe_ep_plan.argtypes = [_vp, _i32, _i32, _i32, _vp, _vp, _vp]
 _lib.moe_ep_dispatch.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp]
 _lib.moe_ep_combine.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i64, _vp,
@@ -83,7 +96,8 @@ _lib.moe_debug_bounded_wait.argtypes = [_u64, _vp]
 for _f in ("moe_router_topk", "moe_permute", "moe_permute_capped", "moe_permute_noalloc", "moe_grouped_ffn",
            "moe_experts_ffn", "moe_combine", "moe_bias_update", "moe_load_stats", "moe_get_status",
            "moe_nvfp4_quantize_weights", "moe_nvfp4_dispatch", "moe_nvfp4_grouped_gemm",
-           "moe_set_wait_timeout_ns", "moe_debug_bounded_wait", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_combine",
+           "moe_int8_quantize_rows", "moe_int8_dispatch", "moe_int8_grouped_gemm", "moe_few_tokens",
+           "moe_few_tokens_int8", "moe_set_wait_timeout_ns", "moe_debug_bounded_wait", "moe_ep_plan", "moe_ep_dispatch", "moe_ep_combine",
            "moe_ipc_handle_bytes", "moe_ipc_get_handle", "moe_ipc_open", "moe_ipc_close"):
     getattr(_lib, _f).restype = _i32
 
@@ -264,6 +278,114 @@ def moe_nvfp4_grouped_gemm(aq, asf, offsets_pad, n_groups: int, rows_cap: int, w
 
 
 # ---------------------------------------------------------------------------
+# 8-bit experts (moe_int8_*) and the layer for a few tokens (moe_few_tokens*)
+# ---------------------------------------------------------------------------
+def _need(fn: str, dtype, *named):
+    """Check (name, tensor, elements) triples: contiguous CUDA tensors of ``dtype`` on the current device
+    with at least that many elements (None passes: the library decides which arguments may be null)."""
+    import torch
+
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for name, t, n in named:
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_cuda or t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
+        if t.dtype is not dtype:
+            raise ValueError(f"{fn}: {name} is {t.dtype}, not {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} is not contiguous")
+        if t.numel() < n:
+            raise ValueError(f"{fn}: {name} has {t.numel()} elements, fewer than {n}")
+
+
+def moe_int8_quantize_rows(x, rows: int, K: int, q, scale, stream=None):
+    import torch
+
+    fn = "moe_int8_quantize_rows"
+    _need(fn, torch.bfloat16, ("x", x, rows * K))
+    _need(fn, torch.int8, ("q", q, rows * K))
+    _need(fn, torch.float32, ("scale", scale, rows))
+    _check(fn, _lib.moe_int8_quantize_rows(_p(x), rows, K, _p(q), _p(scale), _stream(stream)))
+
+
+def moe_int8_dispatch(x, token_row, T: int, d: int, top_k: int, n_rows: int, xq, xs, xq_tok=None, xs_tok=None,
+                      stream=None):
+    import torch
+
+    fn = "moe_int8_dispatch"
+    _need(fn, torch.bfloat16, ("x", x, T * d))
+    _need(fn, torch.int32, ("token_row", token_row, T * top_k))
+    _need(fn, torch.int8, ("xq", xq, n_rows * d), ("xq_tok", xq_tok, T * d))
+    _need(fn, torch.float32, ("xs", xs, n_rows), ("xs_tok", xs_tok, T))
+    _check(fn, _lib.moe_int8_dispatch(_p(x), _p(token_row), T, d, top_k, n_rows, _p(xq), _p(xs), _p(xq_tok),
+                                      _p(xs_tok), _stream(stream)))
+
+
+def moe_int8_grouped_gemm(aq, a_scale, offsets, n_groups: int, n_rows: int, expert_base: int, wq, w_scale, N: int,
+                          K: int, epilogue: int, out, stream=None):
+    import torch
+
+    fn = "moe_int8_grouped_gemm"
+    w_rows = (expert_base + n_groups) * N * (2 if epilogue == MOE_INT8_EPI_SWIGLU else 1)
+    _need(fn, torch.int8, ("aq", aq, n_rows * K), ("wq", wq, w_rows * K))
+    _need(fn, torch.float32, ("a_scale", a_scale, n_rows), ("w_scale", w_scale, w_rows))
+    _need(fn, torch.int32, ("offsets", offsets, n_groups + 1))
+    _need(fn, torch.bfloat16, ("out", out, n_rows * N * (n_groups if offsets is None else 1)))
+    _check(fn, _lib.moe_int8_grouped_gemm(_p(aq), _p(a_scale), _p(offsets), n_groups, n_rows, expert_base, _p(wq),
+                                          _p(w_scale), N, K, epilogue, _p(out), _stream(stream)))
+
+
+def moe_few_tokens_scratch_bytes(T: int, d: int, d_ff: int, n_routed: int, n_shared: int, top_k: int) -> int:
+    return int(_lib.moe_few_tokens_scratch_bytes(T, d, d_ff, n_routed, n_shared, top_k))
+
+
+def _need_few(fn, w_dtype, x, w_router, bias, logit_offset, w1, w2, T, d, d_ff, n_routed, n_shared, top_k, activation,
+              topk_idx, gates, counts, out, scratch, scratch_bytes):
+    import torch
+
+    E = n_routed + n_shared
+    f1 = 2 * d_ff if activation == MOE_ACT_SWIGLU else d_ff
+    _need(fn, torch.bfloat16, ("x", x, T * d), ("w_router", w_router, E * d), ("out", out, T * d))
+    _need(fn, w_dtype, ("w1", w1, E * f1 * d), ("w2", w2, E * d * d_ff))
+    _need(fn, torch.float32, ("bias", bias, n_routed), ("logit_offset", logit_offset, n_routed),
+          ("gates", gates, T * (top_k + n_shared)))
+    _need(fn, torch.int32, ("topk_idx", topk_idx, T * top_k), ("counts", counts, n_routed))
+    _need(fn, torch.uint8, ("scratch", scratch, scratch_bytes))
+
+
+def moe_few_tokens(x, w_router, bias, logit_offset, w1, w2, T: int, d: int, d_ff: int, n_routed: int, n_shared: int,
+                   top_k: int, route_scale: float, activation: int, topk_idx, gates, counts, out, scratch,
+                   scratch_bytes: int, stream=None):
+    import torch
+
+    fn = "moe_few_tokens"
+    _need_few(fn, torch.bfloat16, x, w_router, bias, logit_offset, w1, w2, T, d, d_ff, n_routed, n_shared, top_k,
+              activation, topk_idx, gates, counts, out, scratch, scratch_bytes)
+    _check(fn, _lib.moe_few_tokens(
+        _p(x), _p(w_router), _p(bias), _p(logit_offset), _p(w1), _p(w2), T, d, d_ff, n_routed, n_shared, top_k,
+        route_scale, activation, _p(topk_idx), _p(gates), _p(counts), _p(out), _p(scratch), scratch_bytes,
+        _stream(stream)))
+
+
+def moe_few_tokens_int8(x, w_router, bias, logit_offset, w1, w1_scale, w2, w2_scale, T: int, d: int, d_ff: int,
+                        n_routed: int, n_shared: int, top_k: int, route_scale: float, activation: int, topk_idx,
+                        gates, counts, out, scratch, scratch_bytes: int, stream=None):
+    import torch
+
+    fn = "moe_few_tokens_int8"
+    _need_few(fn, torch.int8, x, w_router, bias, logit_offset, w1, w2, T, d, d_ff, n_routed, n_shared, top_k,
+              activation, topk_idx, gates, counts, out, scratch, scratch_bytes)
+    f1 = 2 * d_ff if activation == MOE_ACT_SWIGLU else d_ff
+    _need(fn, torch.float32, ("w1_scale", w1_scale, (n_routed + n_shared) * f1),
+          ("w2_scale", w2_scale, (n_routed + n_shared) * d))
+    _check(fn, _lib.moe_few_tokens_int8(
+        _p(x), _p(w_router), _p(bias), _p(logit_offset), _p(w1), _p(w1_scale), _p(w2), _p(w2_scale), T, d, d_ff,
+        n_routed, n_shared, top_k, route_scale, activation, _p(topk_idx), _p(gates), _p(counts), _p(out), _p(scratch),
+        scratch_bytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
 # expert parallelism over peer memory (moe_ep_*) and the peer mappings (moe_ipc_*)
 # ---------------------------------------------------------------------------
 def moe_ep_plan(counts_all, rank: int, world: int, n_routed: int, send_base, recv_offsets, stream=None):
@@ -355,20 +477,28 @@ class MoELayer:
     2*d_ff, d], gate rows then up rows), w2 [n_routed + n_shared, d, d_ff] (bf16),
     bias [n_routed] fp32 (updated in place by ``bias_update``).  ``route_scale``
     multiplies the joint routing weights (route_scale x global_scale of the released
-    configuration; 1 keeps them summing to 1).
+    configuration; 1 keeps them summing to 1).  ``precision="nvfp4"`` and ``"int8"``
+    take quantized weights (``set_nvfp4_weights``, ``set_int8_weights``).
+    ``few_tokens=True`` (T <= MOE_FEW_MAX_T, bf16 or int8, no capacity) runs the whole
+    forward as one kernel (moe_few_tokens, moe_few_tokens_int8).
     """
 
     def __init__(self, shape: LayerShape, device="cuda", fused_experts: bool = True, gather_rows: bool = False,
                  capacity_factor: Optional[float] = None, activation: str = "gelu_tanh", route_scale: float = 1.0,
-                 precision: str = "bf16"):
+                 precision: str = "bf16", few_tokens: bool = False):
         import torch
 
         self.shape = s = shape
         # "nvfp4": the routed experts in NVFP4 (W4A4, quantized weights set by set_nvfp4_weights);
         # the router and the shared experts stay bf16
-        if precision not in ("bf16", "nvfp4"):
+        # "int8": all experts in 8-bit codes (W8A8, weights set by set_int8_weights)
+        if precision not in ("bf16", "nvfp4", "int8"):
             raise ValueError(precision)
         self.nvfp4 = precision == "nvfp4"
+        self.int8 = precision == "int8"
+        self.few_tokens = bool(few_tokens)
+        if self.few_tokens and (self.nvfp4 or capacity_factor is not None or s.T > MOE_FEW_MAX_T):
+            raise ValueError("few_tokens needs T <= MOE_FEW_MAX_T, bf16 or int8 experts and no capacity")
         # expert type: GELU MLP (w1 [E, d_ff, d]) or SwiGLU (w1 [E, 2*d_ff, d]: gate rows, then up rows)
         self.activation = {"gelu_tanh": MOE_ACT_GELU_TANH, "swiglu": MOE_ACT_SWIGLU}[activation]
         # multiplier of the joint routing weights (route_scale x global_scale of the released config)
@@ -382,6 +512,16 @@ class MoELayer:
         # moe_permute and loads whole tiles
         self.gather_rows = gather_rows and fused_experts
         dev = torch.device(device)
+        self.w1q = self.w1s = self.w2q = self.w2s = None
+        if self.few_tokens:  # the routing outputs, the result and the kernel's scratch are all it keeps
+            self.topk_idx = torch.empty((s.T, s.top_k), dtype=torch.int32, device=dev)
+            self.gates = torch.empty((s.T, s.top_k + s.n_shared), dtype=torch.float32, device=dev)
+            self.counts = torch.empty((s.n_routed,), dtype=torch.int32, device=dev)
+            self.out = torch.empty((s.T, s.d), dtype=torch.bfloat16, device=dev)
+            self.stats = torch.zeros((4,), dtype=torch.int32, device=dev)
+            self.scratch_bytes = moe_few_tokens_scratch_bytes(s.T, s.d, s.d_ff, s.n_routed, s.n_shared, s.top_k)
+            self.scratch = torch.empty((self.scratch_bytes,), dtype=torch.uint8, device=dev)
+            return
         R = s.T * s.top_k
         bf = torch.bfloat16
         self.topk_idx = torch.empty((s.T, s.top_k), dtype=torch.int32, device=dev)
@@ -389,7 +529,7 @@ class MoELayer:
         self.counts = torch.empty((s.n_routed,), dtype=torch.int32, device=dev)
         self.offsets = torch.empty((s.n_routed + 1,), dtype=torch.int32, device=dev)
         # the bf16 path's copied rows and hidden rows (the NVFP4 path keeps its own FP4 buffers)
-        R_bf16 = 1 if self.nvfp4 else max(R, 1)
+        R_bf16 = 1 if self.nvfp4 or self.int8 else max(R, 1)
         self.x_perm = torch.empty((R_bf16, s.d), dtype=bf, device=dev)
         self.row_token = torch.empty((max(R, 1),), dtype=torch.int32, device=dev)
         self.token_row = torch.empty((s.T, s.top_k), dtype=torch.int32, device=dev)
@@ -403,6 +543,16 @@ class MoELayer:
         self.out = torch.empty((s.T, s.d), dtype=bf, device=dev)
         # moe_load_stats output: max load and dropped assignments (int32), then MaxVio and the drop rate (fp32 bits)
         self.stats = torch.zeros((4,), dtype=torch.int32, device=dev)
+        if self.int8:
+            i8, f32, ns = torch.int8, torch.float32, max(s.n_shared, 1)
+            self.xq = torch.empty((max(R, 1), s.d), dtype=i8, device=dev)
+            self.xs = torch.empty((max(R, 1),), dtype=f32, device=dev)
+            self.xq_tok = torch.empty((s.T, s.d), dtype=i8, device=dev)
+            self.xs_tok = torch.empty((s.T,), dtype=f32, device=dev)
+            # hidden codes of the routed rows, then of the shared experts' rows
+            self.hq = torch.empty((max(R, ns * s.T, 1), s.d_ff), dtype=i8, device=dev)
+            self.hs = torch.empty((max(R, ns * s.T, 1),), dtype=f32, device=dev)
+            self.offsets_shared = (torch.arange(ns + 1, dtype=torch.int32) * s.T).to(dev)
         if self.nvfp4:
             self.rows_cap = moe_nvfp4_rows_capacity(s.T, s.n_routed, s.top_k)
             u8 = torch.uint8
@@ -435,6 +585,58 @@ class MoELayer:
         self.g2 = torch.empty((E,), dtype=torch.float32, device=dev)
         moe_nvfp4_quantize_weights(w1, E, f1, d, self.w1q, self.w1sf, self.g1, stream=stream)
         moe_nvfp4_quantize_weights(w2, E, d, f, self.w2q, self.w2sf, self.g2, stream=stream)
+
+    def set_int8_weights(self, w1, w2, stream=None):
+        """Code every expert's weights (w1 [E, d_ff, d] -- [E, 2*d_ff, d] for SwiGLU -- and w2 [E, d, d_ff],
+        E = n_routed + n_shared) in 8 bits on the device, one scale per output channel; ``forward`` then
+        ignores its w1 and w2 (they may be None)."""
+        import torch
+
+        s = self.shape
+        E, f, d = s.n_routed + s.n_shared, s.d_ff, s.d
+        f1 = 2 * f if self.activation == MOE_ACT_SWIGLU else f
+        dev = w1.device
+        self.w1q = torch.empty((E, f1, d), dtype=torch.int8, device=dev)
+        self.w1s = torch.empty((E, f1), dtype=torch.float32, device=dev)
+        self.w2q = torch.empty((E, d, f), dtype=torch.int8, device=dev)
+        self.w2s = torch.empty((E, d), dtype=torch.float32, device=dev)
+        moe_int8_quantize_rows(w1, E * f1, d, self.w1q, self.w1s, stream=stream)
+        moe_int8_quantize_rows(w2, E * d, f, self.w2q, self.w2s, stream=stream)
+
+    def _forward_int8(self, x, main, ffn_events=None):
+        s = self.shape
+        T, d, f, k, R = s.T, s.d, s.d_ff, s.top_k, s.T * s.top_k
+        epi = MOE_INT8_EPI_SWIGLU if self.activation == MOE_ACT_SWIGLU else MOE_INT8_EPI_GELU
+        moe_int8_dispatch(x, self.token_row, T, d, k, R, self.xq, self.xs, self.xq_tok if s.n_shared else None,
+                          self.xs_tok if s.n_shared else None, stream=main)
+        if ffn_events is not None:
+            ffn_events[0].record(main)
+        # rows past the last expert's (dropped by a capacity) are coded but belong to no group
+        moe_int8_grouped_gemm(self.xq, self.xs, self.offsets, s.n_routed, R, 0, self.w1q, self.w1s, f, d, epi, self.h,
+                              stream=main)
+        moe_int8_quantize_rows(self.h, R, f, self.hq, self.hs, stream=main)
+        moe_int8_grouped_gemm(self.hq, self.hs, self.offsets, s.n_routed, R, 0, self.w2q, self.w2s, d, f,
+                              MOE_INT8_EPI_BF16, self.y_perm, stream=main)
+        if s.n_shared > 0:
+            moe_int8_grouped_gemm(self.xq_tok, self.xs_tok, None, s.n_shared, T, s.n_routed, self.w1q, self.w1s, f, d,
+                                  epi, self.h_shared, stream=main)
+            moe_int8_quantize_rows(self.h_shared, s.n_shared * T, f, self.hq, self.hs, stream=main)
+            moe_int8_grouped_gemm(self.hq, self.hs, self.offsets_shared, s.n_shared, s.n_shared * T, s.n_routed,
+                                  self.w2q, self.w2s, d, f, MOE_INT8_EPI_BF16, self.y_shared, stream=main)
+        if ffn_events is not None:
+            ffn_events[1].record(main)
+
+    def _forward_few(self, x, w_router, w1, w2, bias, logit_offset, main, dst):
+        s = self.shape
+        if self.int8:
+            moe_few_tokens_int8(x, w_router, bias, logit_offset, self.w1q, self.w1s, self.w2q, self.w2s, s.T, s.d,
+                                s.d_ff, s.n_routed, s.n_shared, s.top_k, self.route_scale, self.activation,
+                                self.topk_idx, self.gates, self.counts, dst, self.scratch, self.scratch_bytes,
+                                stream=main)
+        else:
+            moe_few_tokens(x, w_router, bias, logit_offset, w1, w2, s.T, s.d, s.d_ff, s.n_routed, s.n_shared, s.top_k,
+                           self.route_scale, self.activation, self.topk_idx, self.gates, self.counts, dst,
+                           self.scratch, self.scratch_bytes, stream=main)
 
     def _forward_nvfp4(self, x, w1, w2, main, ffn_events=None):
         s = self.shape
@@ -472,7 +674,19 @@ class MoELayer:
         s = self.shape
         main = stream if stream is not None else torch.cuda.current_stream()
         T, d, f, k = s.T, s.d, s.d_ff, s.top_k
-        side = s.n_shared > 0 and not self.fused_experts and not self.nvfp4
+        if self.int8 and self.w1q is None:
+            raise RuntimeError("set_int8_weights() first")
+        if self.few_tokens:
+            if scores_out is not None:
+                raise ValueError("scores_out is not available with few_tokens")
+            dst = self.out if out is None else out
+            if ffn_events is not None:  # one kernel: its events bracket the whole layer
+                ffn_events[0].record(main)
+            self._forward_few(x, w_router, w1, w2, bias, logit_offset, main, dst)
+            if ffn_events is not None:
+                ffn_events[1].record(main)
+            return dst
+        side = s.n_shared > 0 and not self.fused_experts and not self.nvfp4 and not self.int8
         if side:
             # the shared experts need only x: their stream starts with the router, and the
             # dispatch kernels (small, memory-bound) run beside their GEMM tiles
@@ -484,24 +698,26 @@ class MoELayer:
             moe_grouped_ffn(x, None, s.n_shared, T, s.n_routed, w1, w2, d, f, self.activation, self.h_shared,
                             self.y_shared, stream=self.side)
             self.ev_shared.record(self.side)
-        x_perm = None if (self.gather_rows or self.nvfp4) else self.x_perm
+        x_perm = None if (self.gather_rows or self.nvfp4 or self.int8) else self.x_perm
         if self.capacity is None:
             moe_permute(x, self.topk_idx, self.counts, T, d, s.n_routed, k, self.offsets, x_perm, self.row_token,
                         self.token_row, self.scratch, self.scratch_bytes, stream=main)
         else:
             moe_permute_capped(x, self.topk_idx, self.counts, T, d, s.n_routed, k, self.capacity, self.offsets,
                                x_perm, self.row_token, self.token_row, self.scratch, self.scratch_bytes, stream=main)
-        if ffn_events is not None and not self.nvfp4:
+        if ffn_events is not None and not self.nvfp4 and not self.int8:
             ffn_events[0].record(main)
         if self.nvfp4:  # its events bracket the two FP4 GEMMs alone
             self._forward_nvfp4(x, w1, w2, main, ffn_events)
+        elif self.int8:  # its events bracket the products and the coding between them
+            self._forward_int8(x, main, ffn_events)
         elif self.fused_experts:
             moe_experts_ffn(x, x_perm, self.row_token, self.offsets, T, s.n_routed, s.n_shared, k, w1, w2, d, f,
                             self.activation, self.h, self.y_perm, self.y_shared, stream=main)
         else:
             moe_grouped_ffn(self.x_perm, self.offsets, s.n_routed, T * k, 0, w1, w2, d, f, self.activation,
                             self.h, self.y_perm, stream=main)
-        if ffn_events is not None and not self.nvfp4:
+        if ffn_events is not None and not self.nvfp4 and not self.int8:
             ffn_events[1].record(main)
         if side:
             main.wait_event(self.ev_shared)
@@ -513,10 +729,14 @@ class MoELayer:
     # kernels of libmoe launched by one forward + bias update
     def launches_per_step(self) -> int:
         """libmoe kernels one forward + bias update launches."""
+        if self.few_tokens:
+            return 2
         one_chunk = self.shape.T <= 256 and os.environ.get("MOE_PERMUTE_ONE_CHUNK") != "0"
         indices = 1 if one_chunk else 3  # the dispatch's index launches (one CTA when one chunk holds every token)
         if self.nvfp4:  # permute (indices), FP4 dispatch 1, FP4 GEMMs 2, shared bf16 GEMMs 2
             return 1 + indices + 1 + 2 + 2 + 1 + 1
+        if self.int8:  # dispatch 1, GEMM, coding, GEMM for the routed and the shared experts
+            return 1 + indices + 1 + 3 + (3 if self.shape.n_shared > 0 else 0) + 1 + 1
         experts = 2 if self.fused_experts else 4
         permute = indices + (0 if self.gather_rows else 1)
         return 1 + permute + experts + 1 + 1

@@ -1,0 +1,87 @@
+// int8_gemm.cu -- the experts' products in 8-bit codes with a scale for each
+// token (A row) and each output channel (weight row): the grouped GEMM of
+// grouped_gemm.cuh on kind::i8 tensor cores.  The int32 sums are exact, so a
+// result is one product of the two scales and the sum, whatever the tiling.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "grouped_gemm.cuh"
+#include "moe.h"
+#include "moe_internal.h"
+
+using namespace moe;
+using namespace moe::gffn;
+
+extern "C" int moe_int8_grouped_gemm(const int8_t* aq, const float* a_scale, const int32_t* offsets, int n_groups,
+                                     int n_rows, int expert_base, const int8_t* wq, const float* w_scale, int N,
+                                     int K, int epilogue, moe_bf16* out, void* stream) {
+  if (n_groups < 0 || n_rows < 0 || expert_base < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (epilogue != MOE_INT8_EPI_BF16 && epilogue != MOE_INT8_EPI_GELU && epilogue != MOE_INT8_EPI_SWIGLU)
+    return MOE_ERR_INVALID_ARG;
+  if (!aq || !a_scale || !wq || !w_scale || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(aq) || !aligned4(a_scale) || !aligned4(offsets) || !aligned16(wq) || !aligned16(w_scale) ||
+      !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > 131072 || N % 32 != 0 || N > 0x3fffffff || n_groups > MOE_MAX_GROUPS)
+    return MOE_ERR_UNSUPPORTED;
+  if (n_rows == 0 || n_groups == 0) return MOE_OK;
+  const bool identity = offsets == nullptr;
+  const long long out_rows = identity ? (long long)n_groups * n_rows : n_rows;
+  if (out_rows > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+
+  cudaStream_t s = (cudaStream_t)stream;
+  int dev, sms;
+  int rc = device_info(&dev, &sms);
+  if (rc != MOE_OK) return rc;
+  unsigned int* status = status_ptr();
+  if (!status) return MOE_ERR_CUDA;
+
+  const bool swiglu = epilogue == MOE_INT8_EPI_SWIGLU;
+  const int w_rows = swiglu ? 2 * N : N;
+  const bool pair = choose_pair(out_rows, n_groups);
+  const int tile_m = pair ? Cfg<true, 4>::TILE_M : Cfg<false, 4>::TILE_M;
+  const long long tiles_upper = identity ? (long long)n_groups * ((n_rows + tile_m - 1) / tile_m)
+                                         : (n_rows + tile_m - 1) / tile_m + n_groups;
+
+  GemmSpec g{};
+  g.a0 = aq;
+  g.a0_rows = (uint64_t)n_rows;
+  g.b = wq + (size_t)expert_base * w_rows * K;
+  g.b_rows = (uint64_t)w_rows;
+  Params& p = g.p;
+  p.offsets = offsets;
+  p.G_r = identity ? 0 : n_groups;
+  p.G_s = identity ? n_groups : 0;
+  p.routed_rows = n_rows;
+  p.shared_rows = n_rows;
+  p.timeout_ns = wait_timeout_ns();
+  p.status = status;
+  p.hints = hints_for();
+  p.n_major_rows = n_major_rows_for();
+  p.prefetch_kb = prefetch_for();
+  p.a_scale = a_scale;
+  p.b_scale = w_scale + (size_t)expert_base * w_rows;
+  p.b_scale_ld = w_rows;
+  p.C0 = p.C1 = reinterpret_cast<__nv_bfloat16*>(out);
+  p.c0_limit = p.c1_limit = (int)out_rows;
+  p.c1_stride = n_rows;
+  p.N = N;
+  p.K = K;
+  p.n_tiles_n = swiglu ? (N + SWIGLU_OUT - 1) / SWIGLU_OUT : (N + BN - 1) / BN;
+  p.b_up_row = N;
+  p.ldc = N;
+  // the tensor cores do 8-bit work at twice the bf16 rate, so a launch of as many operations is half as long
+  const double flop = (double)out_rows * K * w_rows;
+  const int which = epilogue == MOE_INT8_EPI_BF16 ? 2 : 1;
+  switch (epilogue) {
+    case MOE_INT8_EPI_BF16:
+      return run_gemm<EPI_NONE, true>(g, pair, stages_for(pair, wide_for(pair, EPI_NONE), which, flop), sms,
+                                      tiles_upper, s);
+    case MOE_INT8_EPI_GELU:
+      return run_gemm<EPI_GELU, true>(g, pair, stages_for(pair, wide_for(pair, EPI_GELU), which, flop), sms,
+                                      tiles_upper, s);
+    default:
+      return run_gemm<EPI_SWIGLU, true>(g, pair, stages_for(pair, wide_for(pair, EPI_SWIGLU), which, flop), sms,
+                                        tiles_upper, s);
+  }
+}
