@@ -7,32 +7,35 @@
 // once, (touched + n_shared) * mats * d * d_ff values; everything else is small.
 // So the kernel is a weight stream with the layer's other steps hidden behind it:
 //
-//   weights   A unit of work is 16 rows of one expert matrix (8 gate rows and the
-//             8 matching up rows for SwiGLU), a row's K split over kw warps of a
-//             CTA.  Units of all touched experts are dealt round-robin to the CTAs
-//             (one an SM), so one token's 8 experts spread over every SM where
-//             128-row GEMM tiles would occupy a fraction of them.  Each thread
-//             copies the 16-byte pieces it will itself feed to the tensor core into
-//             a private ring of shared memory (cp.async, NST chunks of 128 bytes of
-//             K by 16 rows a warp: up to 128 KB in flight an SM), so the stream
-//             needs no barrier, and runs on across units, from W1 into W2, and
-//             behind the grid barriers.
+//   items     The weights are cut into items: 16 rows of one expert matrix (8 gate
+//             rows and the 8 matching up rows for SwiGLU) by one of S slices of K.
+//             Every warp of the grid (16 in one CTA an SM) takes the next item by
+//             ticket, so one token's 8 experts keep every SM busy where 128-row
+//             GEMM tiles would fill a fraction of them, and SMs that get more of
+//             HBM's bandwidth do more of the work (with items dealt out in advance
+//             the first SM had read its share after 52 us and the last after 84).
+//   stream    Each warp has a ring of its own in shared memory (NST chunks of 256
+//             bytes of K by 16 rows, 192 KB an SM) that its lane 0 fills by TMA, so
+//             the stream needs no barrier, and runs on across items, from W1 into
+//             W2, and behind the grid barriers.  The loads are marked evict-first:
+//             a weight is read once, and L2 keeps what other kernels left there.
 //   products  mma.sync m16n8k16 bf16 (m16n8k32 s8): weight rows are M, the expert's
 //             tokens N (up to 8 a tile, 8 tiles).  At one to a few tokens an expert
 //             the tensor pipe is almost idle at any instruction's rate, and this form
-//             takes its weights straight from registers: K may be permuted as long
+//             takes its operands straight from registers: K may be permuted as long
 //             as both operands agree, so lane (r, c) holds 16 contiguous bytes of
-//             rows r and r + 8 and of token r, which is exactly what it loads.
+//             rows r and r + 8 and of token r.  Each item leaves fp32 (int32) partial
+//             sums of its slice.
 //   phases    0  router logits, W_r's rows in groups of 16 by KS slices of K over
-//                the CTAs (8-bit: the tokens' codes too); grid barrier
-//                then every CTA selects for all T tokens itself (a warp a token)
-//             1  h = act(W1 x) for every (touched or shared expert, token) row, kept
-//                in fp32 precision: as bf16 high and low parts (the product with
-//                both costs no extra weight traffic), or for 8-bit experts fp32, coded per
-//                row once the row is complete; grid barrier (8-bit: two)
-//             2  y = W2 h in fp32; the CTA that completes a block of 16 output
-//                columns (a counter per block) sums it over the experts in the
-//                contributors' order, so the result does not depend on timing
+//                the CTAs (8-bit: the tokens' codes too); grid barrier, then every
+//                CTA selects for all T tokens itself (a warp a token)
+//             1  items of W1; grid barrier; the slices' sums, activation, and h in
+//                fp32 precision: as bf16 high and low parts (the product with both
+//                costs no extra weight traffic), or for 8-bit experts coded per row;
+//                grid barrier
+//             2  items of W2; grid barrier; out = the sum over the contributors'
+//                slices in a fixed order
+//             While the CTAs meet, HBM goes on with the rings of the next phase.
 //
 // The grid barriers need every CTA resident: the launch is cooperative, and every
 // wait is bounded (wait_timeout_ns, MOE_STATUS_TIMEOUT).
@@ -40,6 +43,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "int8.cuh"
 #include "moe.h"
@@ -51,27 +56,32 @@ namespace few {
 
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
-constexpr int NST = 5;        // ring stages (chunks) per thread
-constexpr int AHEAD = NST - 1;
-constexpr int CHUNK = 128;    // bytes of K of one row a chunk holds
-constexpr int ROWS = 16;      // weight rows of a unit
+constexpr int NST = 3;        // ring stages (chunks) per warp
+constexpr int BOX = 128;      // bytes of K of one row a TMA box holds (one swizzle atom)
+constexpr int CHUNK = 256;    // and a chunk: two boxes side by side
+constexpr int STEPS = CHUNK / 64;  // 64-byte steps of K (two MMA instructions each)
+constexpr int ROWS = 16;      // weight rows of an item
+constexpr int STAGE_BYTES = ROWS * CHUNK;
+constexpr int BOX_BYTES = ROWS * BOX;
 constexpr int NT_MAX = MOE_FEW_MAX_T / 8;
 constexpr int KS_MAX = 8;     // K slices of the router phase
+constexpr int S_MAX = 8;      // K slices of the experts' matrices
 constexpr int E_LD = 272;     // pitch of a token's partial logits
-constexpr int RED_NT = 4;     // token tiles reduced at a time
-constexpr int RED_COL = 20;   // floats per token column of a reduced tile (16 rows, padded: conflict-free)
+constexpr int RED_COL = 20;   // floats per token column of a warp's logits tile (16 rows, padded: conflict-free)
 constexpr int RED_TILE = 8 * RED_COL;
 constexpr int MAX_CONTRIB = MOE_MAX_TOP_K + MOE_MAX_SHARED;
+constexpr int SELECT_ALL_T = 8;
+constexpr int QUEUE = 8;      // a warp's items between their first load and their products
+constexpr int NO_ITEM = 0x7fffffff;
 
 struct Params {
   const uint8_t* x;    // [T, d] bf16
   const uint8_t* w_r;  // [E, d] bf16
   const float* bias;
   const float* offset;
-  const uint8_t* w1;  // [E, f1, d] bf16 or int8
-  const uint8_t* w2;  // [E, d, f]
-  const float* w1s;   // [E, f1] channel scales (int8)
-  const float* w2s;   // [E, d]
+  const float* w1s;  // [E, f1] channel scales (int8)
+  const float* w2s;  // [E, d]
+  int elem;          // bytes of an expert weight
   int T, d, f, n_routed, n_shared, k;
   int swiglu;
   float gate_scale;
@@ -80,38 +90,54 @@ struct Params {
   int32_t* counts;
   __nv_bfloat16* out;
   // scratch
-  unsigned int* bar;       // [4] grid barriers, zero at launch
-  unsigned int* blk_done;  // [d / 16] experts finished per output block, zero at launch
-  float* logits;           // [KS][T][E_LD] partial logits
-  uint8_t* xq;             // [T, d] token codes (int8)
-  float* xs;               // [T]
-  uint8_t* h;              // bf16: [2][R, f] high and low parts; int8: [R, f] fp32
-  uint8_t* hq;             // [R, f] row codes (int8)
-  float* hs;               // [R]
-  float* y;                // [R, d] fp32
-  int ks;                  // K slices of the router phase
-  int kw1, kw2;            // warps a row's K is split over, in phases 1 and 2
+  unsigned int* bar;  // [0 .. 3], [5]: grid barriers, [4] the ticket counter; zero at launch
+  float* logits;      // [KS][T][E_LD] partial logits
+  uint8_t* xq;        // [T, d] token codes (int8)
+  float* xs;          // [T]
+  float* u;           // [S1][R, f1] partial sums of W1 x (int32 for 8-bit experts)
+  uint8_t* h;         // bf16: [2][R, f] high and low parts; int8: [R, f] codes
+  float* hs;          // [R] (int8)
+  float* y;           // [S2][R, d] partial sums of W2 h (int32 for 8-bit experts)
+  int ks;             // K slices of the router phase
+  int s_log[2];       // log2 of the K slices S1, S2
   uint64_t timeout_ns;
   unsigned int* status;
 };
 
+// One of the two phases: its matrices' items.  Item t (of the phase) is slice t % S of block b of the j-th
+// expert, t / S = j * units + b.
+struct Phase {
+  int k_bytes;  // bytes of a row
+  int nbox;     // boxes of a row
+  int units;    // blocks of 16 rows per expert
+  int s_log;
+  int row_mul;  // first row of block b: b * row_mul
+  int up_row;   // gated: rows from a gate row to its up row, else 0
+  int items;    // of all its experts
+};
+
 struct Smem {
-  uint4 ring[NST * 4 * THREADS];
-  float red[WARPS * RED_NT * RED_TILE];  // int32 sums for 8-bit experts
+  uint8_t ring[WARPS][NST][STAGE_BYTES];  // 128-byte swizzle; 1024-byte aligned
+  uint64_t ring_full[WARPS][NST];
+  int queue[WARPS][QUEUE];
+  Phase ph[2];
   unsigned long long mask[MOE_MAX_ROUTED];  // tokens that picked each expert
   float gate[MOE_FEW_MAX_T * MAX_CONTRIB];
-  int pre[MOE_MAX_ROUTED];              // first row of each expert's tokens
+  short cnt[MOE_MAX_ROUTED], pre[MOE_MAX_ROUTED];  // each expert's tokens and their first row
   short list[MOE_MAX_ROUTED];           // touched experts in index order
   short pick[MOE_FEW_MAX_T * MOE_MAX_TOP_K];
-  short row_of[MOE_FEW_MAX_T * MOE_MAX_TOP_K];  // row of each (token, slot)
+  short row_of[MOE_FEW_MAX_T * MOE_MAX_TOP_K];   // row of each (token, slot)
+  short row_exp[MOE_FEW_MAX_T * MOE_MAX_TOP_K];  // each routed row's expert and token
   uint8_t row_tok[MOE_FEW_MAX_T * MOE_MAX_TOP_K];
   int warp_rows[8], warp_touched[8];
   int n_touched;
+  float score[SELECT_ALL_T * E_LD];
+  uint32_t key[SELECT_ALL_T * E_LD];
   int flag[WARPS];
-  float warp_max[WARPS];
   int abort_flag;
 };
-static_assert(sizeof(Smem) + 16 <= 232448, "shared memory per CTA");
+static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory per CTA");
+static_assert(sizeof(float) * WARPS * NT_MAX * RED_TILE <= WARPS * NST * STAGE_BYTES, "the router's sums use the ring");
 
 template <bool I8>
 struct AccT {
@@ -145,8 +171,13 @@ __device__ __forceinline__ void mma_step(T (&c)[4], const uint4& lo, const uint4
   mma(c, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
 }
 
-__device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// The places of a warp's accumulators in its tile of the router's sums.
+__device__ __forceinline__ void red_store(float* red, const float (&c)[4], int lane) {
+  const int r = lane >> 2, col = 2 * (lane & 3);
+  red[col * RED_COL + r] = c[0];
+  red[(col + 1) * RED_COL + r] = c[1];
+  red[col * RED_COL + r + 8] = c[2];
+  red[(col + 1) * RED_COL + r + 8] = c[3];
 }
 
 __device__ __forceinline__ unsigned int ld_acquire(const unsigned int* p) {
@@ -155,12 +186,15 @@ __device__ __forceinline__ unsigned int ld_acquire(const unsigned int* p) {
   return v;
 }
 
-// Every CTA arrives; the CTA goes on when all have.  False when the wait ran out of time.
-__device__ __forceinline__ bool grid_barrier(unsigned int* ctr, const Params& p, Smem* sm) {
+// Grid-wide barrier in two halves: every CTA arrives (its stores before that are visible to CTAs that have
+// waited); the CTA goes on when all have.  The wait returns false when it ran out of time.
+__device__ __forceinline__ void grid_arrive(unsigned int* ctr) {
   __syncthreads();
+  if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(ctr) : "memory");
+}
+
+__device__ __forceinline__ bool grid_wait(unsigned int* ctr, const Params& p, Smem* sm) {
   if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(ctr, 1u);
     const uint64_t t0 = globaltimer();
     for (uint32_t it = 1; ld_acquire(ctr) < gridDim.x; ++it) {
       if ((it & 63u) == 0 && globaltimer() - t0 > p.timeout_ns) {
@@ -169,217 +203,414 @@ __device__ __forceinline__ bool grid_barrier(unsigned int* ctr, const Params& p,
         break;
       }
     }
-    __threadfence();
   }
   __syncthreads();
   return sm->abort_flag == 0;
 }
 
-// What a phase's units look like to a warp.
-struct Phase {
-  const uint8_t* w;   // expert matrices
-  size_t e_bytes;     // bytes of one expert's matrix
-  int k_bytes;        // bytes of a row
-  int nch;            // chunks of a row
-  int units;          // units per expert
-  int row_mul;        // first row of unit b: b * row_mul
-  size_t hi_off;      // bytes from row r to the lane's second row
-  int kw, wk;         // warps a row is split over, this warp's place among them
-  int w0, stride;     // first unit of this warp's worker, workers in the grid
-};
+__device__ __forceinline__ bool grid_barrier(unsigned int* ctr, const Params& p, Smem* sm) {
+  grid_arrive(ctr);
+  return grid_wait(ctr, p, sm);
+}
 
-__device__ __forceinline__ Phase make_phase(const uint8_t* w, int rows, int K, int elem, int kw, bool gated, int f) {
+__device__ __forceinline__ uint4 load16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
+__device__ __forceinline__ Phase make_phase(int rows, int K, int elem, bool gated, int f, int s_log) {
   Phase ph;
-  const int warp = threadIdx.x >> 5;
-  ph.w = w;
   ph.k_bytes = K * elem;
-  ph.e_bytes = (size_t)rows * ph.k_bytes;
-  ph.nch = (ph.k_bytes + CHUNK - 1) / CHUNK;
-  ph.row_mul = gated ? ROWS / 2 : ROWS;
+  ph.nbox = (ph.k_bytes + BOX - 1) / BOX;
   ph.units = gated ? f / (ROWS / 2) : rows / ROWS;
-  ph.hi_off = (size_t)(gated ? f : ROWS / 2) * ph.k_bytes;
-  ph.kw = kw;
-  ph.wk = warp % kw;
-  ph.w0 = (warp / kw) * (int)gridDim.x + (int)blockIdx.x;
-  ph.stride = (WARPS / kw) * (int)gridDim.x;
+  ph.s_log = s_log;
+  ph.row_mul = gated ? ROWS / 2 : ROWS;
+  ph.up_row = gated ? f : 0;
+  ph.items = 0;
   return ph;
 }
 
-// The warp's weight stream: chunk by chunk through its phase-1 units, then its phase-2 units.
-struct Stream {
-  int phase, u, c, stage;
-  bool ready;  // (phase, u) is known and r0 points at it
-  const uint8_t* r0;
+// An item: slice s (boxes lo .. hi - 1) of block b of the j-th expert.
+struct Item {
+  int j, b, s, lo, hi;
 };
+
+__device__ __forceinline__ Item item_at(const Phase& ph, int t) {
+  Item it;
+  it.s = t & ((1 << ph.s_log) - 1);
+  const int u = t >> ph.s_log;
+  it.j = u / ph.units;
+  it.b = u - it.j * ph.units;
+  it.lo = (ph.nbox * it.s) >> ph.s_log;
+  it.hi = (ph.nbox * (it.s + 1)) >> ph.s_log;
+  return it;
+}
 
 __device__ __forceinline__ int expert_at(const Params& p, const Smem* sm, int j) {
   return j < p.n_shared ? p.n_routed + j : sm->list[j - p.n_shared];
 }
 
-__device__ __forceinline__ void stream_point(Stream& s, const Phase& ph, const Params& p, const Smem* sm) {
-  const int j = s.u / ph.units, b = s.u - j * ph.units;
-  const int lane = threadIdx.x & 31;
-  s.r0 = ph.w + (size_t)expert_at(p, sm, j) * ph.e_bytes + (size_t)(b * ph.row_mul + (lane >> 2)) * ph.k_bytes +
-         (lane & 3) * 16;
-  s.ready = true;
-}
+// The warp's weight stream, kept by its lane 0: item by item, two boxes of K at a time.
+struct Stream {
+  int ticket, next;  // the item being loaded (or held), the one drawn for after it
+  int phase;
+  int box, hi;       // next box of the item, its end
+  int row, e;        // the item's first row, and expert
+  int stage, issued, pushed;
+  bool ready;        // the item's place is known
+};
 
-// Find the stream's next unit; n_exp experts are known (before the routing only the shared ones, and the
-// stream then stays within phase 1).
-__device__ __forceinline__ void stream_settle(Stream& s, const Phase& p1, const Phase& p2, int n_exp, bool routed,
-                                              const Params& p, const Smem* sm) {
+// Begin the stream's ticket: phase 1's items come first, then phase 2's.  Before the routing only the first
+// `known` items can be placed; the stream then stops with its ticket in hand.
+__device__ __forceinline__ void stream_begin(Stream& s, int known, const Params& p, Smem* sm) {
   s.ready = false;
-  if (s.phase == 1) {
-    if (s.u < n_exp * p1.units) {
-      stream_point(s, p1, p, sm);
-      return;
-    }
-    if (!routed) return;
-    s.phase = 2;
-    s.u = p2.w0;
-    s.c = p2.wk;
-  }
-  if (s.phase == 2 && s.u < n_exp * p2.units) stream_point(s, p2, p, sm);
+  if (s.ticket >= known) return;
+  const int warp = threadIdx.x >> 5;
+  s.phase = s.ticket < sm->ph[0].items ? 0 : 1;
+  const Phase& ph = sm->ph[s.phase];
+  const int t = s.ticket - (s.phase ? sm->ph[0].items : 0);
+  const bool any = t < ph.items;
+  sm->queue[warp][s.pushed++ & (QUEUE - 1)] = any ? s.ticket : NO_ITEM;
+  if (!any) return;
+  const Item it = item_at(ph, t);
+  s.box = it.lo;
+  s.hi = it.hi;
+  s.row = it.b * ph.row_mul;
+  s.e = expert_at(p, sm, it.j);
+  s.ready = true;
+  s.next = (int)(atomicAdd(p.bar + 4, 1u) + gridDim.x * WARPS);  // every warp's first item is its own number
 }
 
-// Issue the next chunk's copies (none when the stream has ended) and close their group.
-__device__ __forceinline__ void stream_issue(Stream& s, const Phase& p1, const Phase& p2, int n_exp, bool routed,
+// Load the next chunk into the next stage, which the warp has read.
+__device__ __forceinline__ void stream_issue(Stream& s, const CUtensorMap* tm1, const CUtensorMap* tm2, int known,
                                              const Params& p, Smem* sm) {
-  if (s.ready) {
-    const bool one = s.phase == 1;
-    const int k_bytes = one ? p1.k_bytes : p2.k_bytes;
-    const size_t hi_off = one ? p1.hi_off : p2.hi_off;
-    const int off = s.c * CHUNK;
-    const uint32_t dst = smem_u32(&sm->ring[(size_t)s.stage * 4 * THREADS + threadIdx.x]);
-    constexpr uint32_t step = THREADS * 16;
-    cp_async_16(dst, s.r0 + off);
-    cp_async_16(dst + step, s.r0 + hi_off + off);
-    // a row of an odd number of 64-byte halves ends in a half chunk: its second half is zeros
-    const bool second = off + 64 < k_bytes;
-    const uint8_t* src = s.r0 + off + (second ? 64 : 0);
-    cp_async_16_zfill(dst + 2 * step, src, second ? 16 : 0);
-    cp_async_16_zfill(dst + 3 * step, src + hi_off, second ? 16 : 0);
-    s.c += one ? p1.kw : p2.kw;
-    if (s.c >= (one ? p1.nch : p2.nch)) {
-      s.c = one ? p1.wk : p2.wk;
-      s.u += one ? p1.stride : p2.stride;
-      stream_settle(s, p1, p2, n_exp, routed, p, sm);
-    }
+  if (!s.ready || *(volatile int*)&sm->abort_flag) return;
+  const CUtensorMap* map = s.phase == 0 ? tm1 : tm2;
+  const int warp = threadIdx.x >> 5, up_row = sm->ph[s.phase].up_row;
+  uint8_t* dst = sm->ring[warp][s.stage];
+  uint64_t* bar = &sm->ring_full[warp][s.stage];
+  const int n = min(CHUNK / BOX, s.hi - s.box);
+  const uint64_t pol = l2_policy_evict_first();
+  mbar_arrive_expect_tx(bar, n * BOX_BYTES);
+  for (int h = 0; h < n; ++h) {  // K past the row's end reads zeros
+    const int x = (s.box + h) * BOX >> (p.elem - 1);
+    tma_load_3d_hint(dst + h * BOX_BYTES, map, bar, x, s.row, s.e, pol);
+    if (up_row != 0) tma_load_3d_hint(dst + h * BOX_BYTES + BOX_BYTES / 2, map, bar, x, s.row + up_row, s.e, pol);
   }
-  cp_async_commit();
+  ++s.issued;
   s.stage = s.stage + 1 == NST ? 0 : s.stage + 1;
+  s.box += n;
+  if (s.box >= s.hi) {
+    s.ticket = s.next;
+    stream_begin(s, known, p, sm);
+  }
 }
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+// The consuming side, the same in every lane: the next chunk's stage and its phase bit, the next item's place in
+// the queue.
+struct Taken {
+  int stage;
+  uint32_t phase;
+  int head;
+};
 
-__device__ __forceinline__ void group_sync(int group, int kw) {
-  if (kw == 1)
-    __syncwarp();
-  else
-    named_bar_sync(1 + group, kw * 32);
-}
-
-// The places of a warp's accumulators in its part of the reduction buffer.
-template <class T>
-__device__ __forceinline__ void red_store(T* red, const T (&c)[4], int lane) {
-  const int r = lane >> 2, col = 2 * (lane & 3);
-  red[col * RED_COL + r] = c[0];
-  red[(col + 1) * RED_COL + r] = c[1];
-  red[col * RED_COL + r + 8] = c[2];
-  red[(col + 1) * RED_COL + r + 8] = c[3];
-}
-
-template <class T>
-__device__ __forceinline__ T red_sum(const T* red, int kw, int at) {
-  T v = red[at];
-  for (int w = 1; w < kw; ++w) v += red[w * RED_NT * RED_TILE + at];
-  return v;
-}
-
-// One unit: this warp's chunks of 16 weight rows against the expert's n_e token rows, NT tiles of 8, then the
-// sum over the group's warps, handed to epi(column, row, value, value of row + 8) for columns < n_e and
-// rows 0..7.  b_base + row(col) * k_bytes is a token row; PARTS > 1: further parts b_part bytes apart.
-template <class T, int NT, int PARTS, class RowFn, class EpiFn, class NextFn>
-__device__ __forceinline__ void unit(const Phase& ph, int n_e, const uint8_t* b_base, size_t b_part, RowFn row_of_col,
-                                     int& stage, Smem* sm, NextFn next, EpiFn epi) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint8_t* bp[NT];
+// An item's products: its boxes of 16 weight rows against the expert's n_e token rows, NT tiles of 8.
+// b_base + row_of_col(col) * k_bytes is a token row; PARTS > 1: further parts b_part bytes apart.  False when
+// the call has run out of time.
+template <class T, int NT, int PARTS, class RowFn, class NextFn>
+__device__ __forceinline__ bool item_products(T (&acc)[NT][4], int k_bytes, const Item& it, int n_e,
+                                              const uint8_t* b_base, size_t b_part, RowFn row_of_col, Taken& tk,
+                                              const Params& p, Smem* sm, NextFn next) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = lane >> 2, c4 = lane & 3;
+  // 16-byte piece q of row r lies at piece q ^ (r % 8) of the row's 128 bytes
+  const int at0 = r * BOX + ((c4 ^ r) << 4), at1 = r * BOX + (((c4 + 4) ^ r) << 4);
+  constexpr uint32_t NONE = 0xffffffffu;
+  uint32_t bp[NT];  // the lane's token rows as offsets (at most 64 MB)
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int col = j * 8 + (lane >> 2);
-    bp[j] = col < n_e ? b_base + (size_t)row_of_col(col) * ph.k_bytes + (lane & 3) * 16 : nullptr;
+    const int col = j * 8 + r;
+    bp[j] = col < n_e ? (uint32_t)row_of_col(col) * (uint32_t)k_bytes + c4 * 16 : NONE;
+    acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0;
   }
-  T acc[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0;
   constexpr bool EARLY = NT * PARTS <= 2;  // few enough to hold: the token loads go out before the wait
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int c = ph.wk; c < ph.nch; c += ph.kw) {
-    const int off = c * CHUNK;
-    const bool second = off + 64 < ph.k_bytes;
-    uint4 b[EARLY ? NT * PARTS : 1][2];
+  for (int box = it.lo; box < it.hi; box += CHUNK / BOX) {
+    const int off = box * BOX, end = min(k_bytes, it.hi * BOX);
+    // a token's 16 bytes of step i; zeros past the slice, where the stage holds an older chunk's weights
+    auto token = [&](int j, int q, int i) {
+      return bp[j] != NONE && off + i * 64 < end ? load16(b_base + q * b_part + (bp[j] + off + i * 64)) : zero;
+    };
+    uint4 b[EARLY ? NT * PARTS : 1][STEPS];
     if (EARLY) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q) {
-          b[j * PARTS + q][0] = bp[j] ? load16(bp[j] + q * b_part + off) : zero;
-          b[j * PARTS + q][1] = bp[j] && second ? load16(bp[j] + q * b_part + off + 64) : zero;
-        }
+        for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) b[j * PARTS + q][i] = token(j, q, i);
     }
-    cp_async_wait<AHEAD - 1>();
-    const uint4* slot = &sm->ring[(size_t)stage * 4 * THREADS + tid];
-    const uint4 lo0 = slot[0], hi0 = slot[THREADS], lo1 = slot[2 * THREADS], hi1 = slot[3 * THREADS];
-    stage = stage + 1 == NST ? 0 : stage + 1;
-    next();
+    if (!__all_sync(0xffffffffu, mbar_wait(&sm->ring_full[warp][tk.stage], tk.phase, p.timeout_ns, &sm->abort_flag,
+                                           p.status)))
+      return false;
+    const uint8_t* slot = sm->ring[warp][tk.stage];
+    const bool two = box + 1 < it.hi;  // the second box is there
+    uint4 lo[STEPS], hi[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const uint8_t* at = slot + (i >> 1) * BOX_BYTES + ((i & 1) ? at1 : at0);
+      lo[i] = i < 2 || two ? load16(at) : zero;
+      hi[i] = i < 2 || two ? load16(at + 8 * BOX) : zero;
+    }
+    if (++tk.stage == NST) {
+      tk.stage = 0;
+      tk.phase ^= 1u;
+    }
+    __syncwarp();  // every lane has its pieces: the stage may be filled again
+    if (lane == 0) next();
+    __syncwarp();
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {
-        uint4 b0, b1;
-        if (EARLY) {
-          b0 = b[j * PARTS + q][0];
-          b1 = b[j * PARTS + q][1];
-        } else {
-          b0 = bp[j] ? load16(bp[j] + q * b_part + off) : zero;
-          b1 = bp[j] && second ? load16(bp[j] + q * b_part + off + 64) : zero;
-        }
-        mma_step(acc[j], lo0, hi0, b0);
-        mma_step(acc[j], lo1, hi1, b1);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+          mma_step(acc[j], lo[i], hi[i], EARLY ? b[j * PARTS + q][i] : token(j, q, i));
       }
     }
   }
-  const int group = warp / ph.kw;
-  T* red = reinterpret_cast<T*>(sm->red);
-  T* mine = red + warp * RED_NT * RED_TILE;
-  const T* base = red + group * ph.kw * RED_NT * RED_TILE;
-  const int g_tid = ph.wk * 32 + lane;
-#pragma unroll
-  for (int j0 = 0; j0 < NT; j0 += RED_NT) {
-    if (j0 * 8 >= n_e) break;
-    if (j0 > 0) group_sync(group, ph.kw);
-#pragma unroll
-    for (int j = j0; j < NT && j < j0 + RED_NT; ++j) red_store(mine + (j - j0) * RED_TILE, acc[j], lane);
-    group_sync(group, ph.kw);
-    const int cols = min(n_e - j0 * 8, RED_NT * 8);
-    for (int i = g_tid; i < cols * 8; i += ph.kw * 32) {
-      const int col = i >> 3, r = i & 7;
-      const int at = (col >> 3) * RED_TILE + (col & 7) * RED_COL + r;
-      epi(j0 * 8 + col, r, red_sum(base, ph.kw, at), red_sum(base, ph.kw, at + 8));
-    }
-  }
-  group_sync(group, ph.kw);
+  return true;
 }
 
-template <class T, int PARTS, class RowFn, class EpiFn, class NextFn>
-__device__ __forceinline__ void unit_any(const Phase& ph, int n_e, const uint8_t* b_base, size_t b_part,
-                                         RowFn row_of_col, int& stage, Smem* sm, NextFn next, EpiFn epi) {
-  if (n_e <= 8)
-    unit<T, 1, PARTS>(ph, n_e, b_base, b_part, row_of_col, stage, sm, next, epi);
-  else if (n_e <= 16)
-    unit<T, 2, PARTS>(ph, n_e, b_base, b_part, row_of_col, stage, sm, next, epi);
-  else
-    unit<T, NT_MAX, PARTS>(ph, n_e, b_base, b_part, row_of_col, stage, sm, next, epi);
+// Take this warp's items of phase PH and leave their sums at dst[(slice * R + row) * ld + column], column b's 16 rows
+// (gated: gate rows at b * 8, up rows ph.up_row on).
+template <class T, int PH, int PARTS, class NextFn>
+__device__ __forceinline__ void run_items(const Params& p, const uint8_t* b_base, size_t b_part, T* dst, int ld, int R,
+                                          Taken& tk, Smem* sm, NextFn next) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Phase& ph = sm->ph[PH];
+  const int base = PH == 0 ? 0 : sm->ph[0].items;
+  const int hi_col = ph.up_row != 0 ? ph.up_row : ROWS / 2;
+  for (;;) {
+    __syncwarp();
+    const int ticket = sm->queue[warp][tk.head & (QUEUE - 1)];
+    if (ticket - base >= ph.items) return;  // the next phase's, or none
+    ++tk.head;
+    const Item it = item_at(ph, ticket - base);
+    const bool shared = it.j < p.n_shared;
+    const int e = expert_at(p, sm, it.j);
+    const int n_e = shared ? p.T : sm->cnt[e];
+    const int row0 = shared ? p.T * p.k + it.j * p.T : sm->pre[e];
+    auto row = [&](int col) { return PH == 0 ? (shared ? col : (int)sm->row_tok[row0 + col]) : row0 + col; };
+    T* to = dst + ((size_t)it.s * R + row0) * ld + it.b * ph.row_mul + (lane >> 2);
+    auto go = [&](auto n_tiles) {
+      constexpr int NT = decltype(n_tiles)::value;
+      T acc[NT][4];
+      if (!item_products<T, NT, PARTS>(acc, ph.k_bytes, it, n_e, b_base, b_part, row, tk, p, sm, next)) return false;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int col = j * 8 + 2 * (lane & 3) + q;
+          if (col < n_e) {
+            to[(size_t)col * ld] = acc[j][q];
+            to[(size_t)col * ld + hi_col] = acc[j][q + 2];
+          }
+        }
+      return true;
+    };
+    bool ok;
+    if (n_e <= 8)
+      ok = go(std::integral_constant<int, 1>{});
+    else if (n_e <= 16)
+      ok = go(std::integral_constant<int, 2>{});
+    else if (n_e <= 32)
+      ok = go(std::integral_constant<int, 4>{});
+    else
+      ok = go(std::integral_constant<int, NT_MAX>{});
+    if (!ok) return;
+  }
+}
+
+// A hidden row's expert and token.
+__device__ __forceinline__ void row_owner(const Params& p, const Smem* sm, int r, int& e, int& t) {
+  if (r < p.T * p.k) {
+    e = sm->row_exp[r];
+    t = sm->row_tok[r];
+  } else {
+    const int q = r - p.T * p.k;
+    e = p.n_routed + q / p.T;
+    t = q % p.T;
+  }
+}
+
+// Four neighbouring columns of W1 x for row r: the slices' sums in order, scaled for 8-bit experts.
+template <bool I8>
+__device__ __forceinline__ void u_at(const Params& p, int R, int f1, int r, int c, float xs, const float* ws,
+                                     float (&v)[4]) {
+  using T = typename AccT<I8>::type;
+  const int S = 1 << p.s_log[0];
+  const uint4* at = reinterpret_cast<const uint4*>(p.u + (size_t)r * f1 + c);
+  T a[4] = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < S; ++s) {
+    const uint4 w = __ldcg(at + (size_t)s * R * f1 / 4);
+    if constexpr (I8) {
+      a[0] += (int)w.x;
+      a[1] += (int)w.y;
+      a[2] += (int)w.z;
+      a[3] += (int)w.w;
+    } else {
+      a[0] += __uint_as_float(w.x);
+      a[1] += __uint_as_float(w.y);
+      a[2] += __uint_as_float(w.z);
+      a[3] += __uint_as_float(w.w);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = I8 ? (float)a[i] * (xs * __ldg(ws + c + i)) : (float)a[i];
+}
+
+template <bool I8>
+__device__ __forceinline__ void h_at(const Params& p, int R, int r, int c, float xs, const float* ws, float (&h)[4]) {
+  const int f1 = p.swiglu ? 2 * p.f : p.f;
+  u_at<I8>(p, R, f1, r, c, xs, ws, h);
+  if (p.swiglu) {
+    float up[4];
+    u_at<I8>(p, R, f1, r, p.f + c, xs, ws, up);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = silu_f32(h[i]) * up[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = gelu_tanh_exp_f32(h[i]);
+  }
+}
+
+// h = act(W1 x) as bf16 high and low parts, four columns a thread over the whole grid.
+__device__ __forceinline__ void finish_hidden(const Params& p, int R) {
+  const int nv = p.f / 4;
+  for (int i = (int)(threadIdx.x * gridDim.x + blockIdx.x); i < R * nv; i += THREADS * (int)gridDim.x) {
+    const int r = i / nv, c = (i - r * nv) * 4;
+    float h[4];
+    h_at<false>(p, R, r, c, 0.0f, nullptr, h);
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      hi[q] = pack_bf16x2(h[2 * q], h[2 * q + 1]);
+      float a = h[2 * q] - __uint_as_float(hi[q] << 16), b = h[2 * q + 1] - __uint_as_float(hi[q] & 0xffff0000u);
+      // an infinite or NaN high part has no low part
+      lo[q] = pack_bf16x2(a - a == 0.0f ? a : 0.0f, b - b == 0.0f ? b : 0.0f);
+    }
+    uint2* to = reinterpret_cast<uint2*>(p.h + ((size_t)r * p.f + c) * 2);
+    *to = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(to) + (size_t)R * p.f * 2) = make_uint2(lo[0], lo[1]);
+  }
+}
+
+// 8-bit experts: a CTA a row, whose values stay in registers between their maximum and their codes (rows past
+// 4 * HV * THREADS values are computed a second time).
+__device__ __forceinline__ void code_hidden(const Params& p, Smem* sm, int R) {
+  constexpr int HV = 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nv = p.f / 4, f1 = p.swiglu ? 2 * p.f : p.f;
+  for (int r = (int)blockIdx.x; r < R; r += (int)gridDim.x) {
+    int e, t;
+    row_owner(p, sm, r, e, t);
+    const float xs = __ldcg(p.xs + t);
+    const float* ws = p.w1s + (size_t)e * f1;
+    // |v| as integers: NaN and infinity stay the largest
+    auto top = [](const float (&v)[4]) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+      return m;
+    };
+    uint32_t m = 0;
+    float keep[HV][4];
+#pragma unroll
+    for (int i = 0; i < HV; ++i)
+      if (tid + i * THREADS < nv) {
+        h_at<true>(p, R, r, (tid + i * THREADS) * 4, xs, ws, keep[i]);
+        m = max(m, top(keep[i]));
+      }
+    for (int c = tid + HV * THREADS; c < nv; c += THREADS) {
+      float v[4];
+      h_at<true>(p, R, r, c * 4, xs, ws, v);
+      m = max(m, top(v));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) sm->flag[warp] = (int)m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) m = max(m, (uint32_t)sm->flag[w]);
+    const q8::RowScale rs = q8::row_scale(__uint_as_float(m));
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.h + (size_t)r * p.f);
+#pragma unroll
+    for (int i = 0; i < HV; ++i)
+      if (tid + i * THREADS < nv) dst[tid + i * THREADS] = q8::code4_f32(keep[i], rs);
+    for (int c = tid + HV * THREADS; c < nv; c += THREADS) {
+      float v[4];
+      h_at<true>(p, R, r, c * 4, xs, ws, v);
+      dst[c] = q8::code4_f32(v, rs);
+    }
+    if (tid == 0) p.hs[r] = rs.scale;
+    __syncthreads();
+  }
+}
+
+// out[t, col] = sum over the contributors of gate * (sum of the slices).  A thread takes one contributor's four
+// neighbouring columns, GL threads (a power of two) one token's contributors, added up in a fixed tree.  (Short code: it
+// runs once, and instructions that are fetched for one use cost more than the loads they issue.)
+template <bool I8>
+__device__ __forceinline__ void finish_out(const Params& p, const Smem* sm, int R) {
+  const int G = p.k + p.n_shared, S = 1 << p.s_log[1];
+  const int gl = G > 8 ? 4 : G > 4 ? 3 : G > 2 ? 2 : G > 1 ? 1 : 0;  // log2 GL
+  const int nv = p.d / 4, total = (p.T * nv) << gl;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint4* y = reinterpret_cast<const uint4*>(p.y);
+  // whole warps: 32 / GL vectors each, neighbouring warps on neighbouring SMs
+  for (int i0 = (warp * (int)gridDim.x + (int)blockIdx.x) * 32; i0 < total; i0 += THREADS * (int)gridDim.x) {
+    const int i = i0 + lane;
+    const int q = i & ((1 << gl) - 1), v = i >> gl;
+    const int t = v / nv, c = v - t * nv;
+    float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (q < G && i < total) {
+      const int r = q < p.k ? (int)sm->row_of[t * MOE_MAX_TOP_K + q] : p.T * p.k + (q - p.k) * p.T + t;
+      const float g = sm->gate[t * MAX_CONTRIB + q];
+      if constexpr (I8) {
+        const int e = q < p.k ? (int)sm->pick[t * MOE_MAX_TOP_K + q] : p.n_routed + q - p.k;
+        const float4 w = __ldg(reinterpret_cast<const float4*>(p.w2s + (size_t)e * p.d) + c);
+        const float hs = __ldcg(p.hs + r);
+        int n[4] = {0, 0, 0, 0};
+#pragma unroll 4
+        for (int s = 0; s < S; ++s) {
+          const uint4 u = __ldcg(y + ((size_t)s * R + r) * nv + c);
+          n[0] += (int)u.x;
+          n[1] += (int)u.y;
+          n[2] += (int)u.z;
+          n[3] += (int)u.w;
+        }
+        a[0] = g * ((float)n[0] * (hs * w.x));
+        a[1] = g * ((float)n[1] * (hs * w.y));
+        a[2] = g * ((float)n[2] * (hs * w.z));
+        a[3] = g * ((float)n[3] * (hs * w.w));
+      } else {
+#pragma unroll 4
+        for (int s = 0; s < S; ++s) {
+          const uint4 u = __ldcg(y + ((size_t)s * R + r) * nv + c);
+          a[0] += __uint_as_float(u.x);
+          a[1] += __uint_as_float(u.y);
+          a[2] += __uint_as_float(u.z);
+          a[3] += __uint_as_float(u.w);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) a[x] *= g;
+      }
+    }
+    for (int o = (1 << gl) >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) a[x] += __shfl_xor_sync(0xffffffffu, a[x], o);
+    if (q == 0 && i < total)
+      *reinterpret_cast<uint2*>(p.out + (size_t)t * p.d + c * 4) =
+          make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+  }
 }
 
 // Phase 0: partial logits of 16 router rows over one slice of K, all tokens.
@@ -387,7 +618,7 @@ __device__ __forceinline__ void router_partial(const Params& p, Smem* sm) {
   const int E = p.n_routed + p.n_shared;
   const int rg_n = (E + ROWS - 1) / ROWS;
   const int k_bytes = p.d * 2;
-  const int nch = (k_bytes + CHUNK - 1) / CHUNK;
+  const int nch = (k_bytes + BOX - 1) / BOX;  // 128-byte pieces of K
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nt = (p.T + 7) / 8;
   const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -401,7 +632,7 @@ __device__ __forceinline__ void router_partial(const Params& p, Smem* sm) {
 #pragma unroll
     for (int j = 0; j < NT_MAX; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
     for (int c = c_lo + warp; c < c_hi; c += WARPS) {
-      const int off = c * CHUNK;
+      const int off = c * BOX;
       const bool second = off + 64 < k_bytes;
       const uint4 lo0 = load16(a0 + off), hi0 = load16(a1 + off);
       const uint4 lo1 = second ? load16(a0 + off + 64) : zero, hi1 = second ? load16(a1 + off + 64) : zero;
@@ -417,23 +648,22 @@ __device__ __forceinline__ void router_partial(const Params& p, Smem* sm) {
         }
       }
     }
+    // the sum over the warps, through the ring's memory (the stream has not begun)
+    float* red = reinterpret_cast<float*>(sm->ring);
 #pragma unroll
-    for (int j0 = 0; j0 < NT_MAX; j0 += RED_NT) {
-      if (j0 < nt) {
+    for (int j = 0; j < NT_MAX; ++j)
+      if (j < nt) red_store(red + (warp * NT_MAX + j) * RED_TILE, acc[j], lane);
+    __syncthreads();
+    for (int i = tid; i < p.T * ROWS; i += THREADS) {
+      const int col = i >> 4, r = i & 15;
+      const int e = rg * ROWS + r;
+      const float* at = red + (col >> 3) * RED_TILE + (col & 7) * RED_COL + r;
+      float v = 0.0f;
 #pragma unroll
-        for (int j = j0; j < j0 + RED_NT; ++j)
-          red_store(sm->red + warp * RED_NT * RED_TILE + (j - j0) * RED_TILE, acc[j], lane);
-        __syncthreads();
-        const int cols = min(p.T - j0 * 8, RED_NT * 8);
-        for (int i = tid; i < cols * ROWS; i += THREADS) {
-          const int col = i >> 4, r = i & 15;
-          const int e = rg * ROWS + r;
-          const float v = red_sum(sm->red, WARPS, (col >> 3) * RED_TILE + (col & 7) * RED_COL + r);
-          if (e < E) p.logits[((size_t)ks * p.T + j0 * 8 + col) * E_LD + e] = v;
-        }
-        __syncthreads();
-      }
+      for (int w = 0; w < WARPS; ++w) v += at[w * NT_MAX * RED_TILE];
+      if (e < E) p.logits[((size_t)ks * p.T + col) * E_LD + e] = v;
     }
+    __syncthreads();
   }
 }
 
@@ -466,118 +696,109 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Select for token t with one warp: scores, k rounds of a warp-wide maximum (the lower index on equal
-// scores), joint gates with the denominator summed in ascending expert index.
-__device__ __forceinline__ void select_token(const Params& p, Smem* sm, int t, bool write) {
-  const int lane = threadIdx.x & 31;
+// Scores of `n` tokens from t0 on, a thread an expert of a token at a time: the logits' slices in order, and the
+// selection's order keys.
+__device__ __forceinline__ void score_tokens(const Params& p, Smem* sm, int t0, int n) {
   const int E = p.n_routed + p.n_shared;
-  constexpr int PER = (MOE_MAX_ROUTED + MOE_MAX_SHARED + 31) / 32;
-  float s[PER];
-  uint32_t key[PER];
+  for (int i = threadIdx.x; i < n * E; i += THREADS) {
+    const int tl = i / E, e = i - tl * E;
+    const float* z = p.logits + (size_t)(t0 + tl) * E_LD + e;
+    float part[KS_MAX];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = i * 32 + lane;
-    s[i] = 0.0f;
-    key[i] = 0;
-    if (e < E) {
-      float z = 0.0f;
-      for (int q = 0; q < p.ks; ++q) z += __ldcg(p.logits + ((size_t)q * p.T + t) * E_LD + e);
-      if (e < p.n_routed) {
-        if (p.offset) z += __ldg(p.offset + e);
-        s[i] = sigmoid_f32(z);
-        key[i] = order_key(s[i] + __ldg(p.bias + e));
-      } else {
-        s[i] = sigmoid_f32(z);
-      }
+    for (int q = 0; q < KS_MAX; ++q) {
+      part[q] = 0.0f;
+      if (q < p.ks) part[q] = __ldcg(z + (size_t)q * p.T * E_LD);
     }
-  }
-  float sc[MOE_MAX_TOP_K];
-  int id[MOE_MAX_TOP_K];
+    const bool routed = e < p.n_routed;
+    const float bias = routed ? __ldg(p.bias + e) : 0.0f;
+    float off = 0.0f;
+    if (routed && p.offset) off = __ldg(p.offset + e);
+    float v = part[0];
 #pragma unroll
-  for (int q = 0; q < MOE_MAX_TOP_K; ++q) {
-    id[q] = 0x7fffffff;
-    sc[q] = 0.0f;
-    if (q < p.k) {
-      uint32_t best = 0;
-      int e = 0x7fffffff;
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (key[i] > best) {  // strictly: the lane's lowest index among equals
-          best = key[i];
-          e = i * 32 + lane;
-        }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)e : 0x7fffffffu);
-      float mine = 0.0f;
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i * 32 + lane == e) {
-          mine = s[i];
-          key[i] = 0;
-        }
-      id[q] = e;
-      sc[q] = __shfl_sync(0xffffffffu, mine, e & 31);
-    }
-  }
-  float den = 0.0f;
-  int prev = -1;
-#pragma unroll
-  for (int q = 0; q < MOE_MAX_TOP_K; ++q) {
-    if (q < p.k) {
-      int next = 0x7fffffff;
-      float ns = 0.0f;
-#pragma unroll
-      for (int r = 0; r < MOE_MAX_TOP_K; ++r)
-        if (id[r] > prev && id[r] < next) {
-          next = id[r];
-          ns = sc[r];
-        }
-      den += ns;
-      prev = next;
-    }
-  }
-  float sh[MOE_MAX_SHARED];
-#pragma unroll
-  for (int q = 0; q < MOE_MAX_SHARED; ++q) {
-    sh[q] = 0.0f;
-    if (q < p.n_shared) {
-      const int e = p.n_routed + q;
-      float mine = 0.0f;
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i * 32 + lane == e) mine = s[i];
-      sh[q] = __shfl_sync(0xffffffffu, mine, e & 31);
-      den += sh[q];
-    }
-  }
-  if (lane == 0) {
-    const int G = p.k + p.n_shared;
-#pragma unroll
-    for (int q = 0; q < MOE_MAX_TOP_K; ++q)
-      if (q < p.k) {
-        const float g = __fmul_rn(__fdiv_rn(sc[q], den), p.gate_scale);
-        sm->gate[t * MAX_CONTRIB + q] = g;
-        sm->pick[t * MOE_MAX_TOP_K + q] = (short)id[q];
-        atomicOr(&sm->mask[id[q]], 1ull << t);
-        if (write) {
-          p.topk_idx[t * p.k + q] = id[q];
-          p.gates[t * G + q] = g;
-        }
-      }
-#pragma unroll
-    for (int q = 0; q < MOE_MAX_SHARED; ++q)
-      if (q < p.n_shared) {
-        const float g = __fmul_rn(__fdiv_rn(sh[q], den), p.gate_scale);
-        sm->gate[t * MAX_CONTRIB + p.k + q] = g;
-        if (write) p.gates[t * G + p.k + q] = g;
-      }
+    for (int q = 1; q < KS_MAX; ++q) v += part[q];
+    const float s = sigmoid_f32(v + off);
+    sm->score[tl * E_LD + e] = s;
+    sm->key[tl * E_LD + e] = routed ? order_key(s + bias) : 0u;
   }
 }
 
-// The routing tables of all tokens, built by every CTA for itself.
-__device__ __forceinline__ void route_all(const Params& p, Smem* sm) {
+// Select for token t (scores at tl) with one warp: k rounds of a warp-wide maximum (the lower index on equal
+// scores), joint gates with the denominator summed in ascending expert index.
+__device__ __forceinline__ void select_token(const Params& p, Smem* sm, int tl, int t, bool write) {
+  const int lane = threadIdx.x & 31;
+  const int G = p.k + p.n_shared;
+  constexpr int PER = MOE_MAX_ROUTED / 32;
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = i * 32 + lane < p.n_routed ? sm->key[tl * E_LD + i * 32 + lane] : 0u;
+  // lane q < k: the q-th pick; then the shared experts
+  int id = lane < G ? p.n_routed + lane - p.k : 0x7fffffff;
+#pragma unroll 1
+  for (int q = 0; q < p.k; ++q) {
+    uint32_t best = 0;
+    int e = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (key[i] > best) {  // strictly: the lane's lowest index among equals
+        best = key[i];
+        e = i * 32 + lane;
+      }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const int win = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)e : 0x7fffffffu);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * 32 + lane == win) key[i] = 0;
+    if (lane == q) id = win;
+  }
+  const float sc = lane < G ? sm->score[tl * E_LD + id] : 0.0f;
+  int rank = 0;
+#pragma unroll 1
+  for (int q = 0; q < G; ++q) rank += __shfl_sync(0xffffffffu, id, q) < id;
+  float den = 0.0f;
+#pragma unroll 1
+  for (int r = 0; r < G; ++r) {
+    const uint32_t who = __ballot_sync(0xffffffffu, lane < G && rank == r);
+    den += __shfl_sync(0xffffffffu, sc, __ffs(who) - 1);
+  }
+  if (lane < G) {
+    const float g = __fmul_rn(__fdiv_rn(sc, den), p.gate_scale);
+    sm->gate[t * MAX_CONTRIB + lane] = g;
+    if (write) p.gates[t * G + lane] = g;
+    if (lane < p.k) {
+      sm->pick[t * MOE_MAX_TOP_K + lane] = (short)id;
+      if (write) p.topk_idx[t * p.k + lane] = id;
+    }
+  }
+}
+
+// The routing tables of all tokens, built by every CTA for itself.  Up to SELECT_ALL_T tokens every CTA also makes the
+// whole selection; more are shared among the CTAs, which then meet again (another barrier costs less than the
+// other tokens' selections).  False when that barrier ran out of time.
+__device__ __forceinline__ bool route_all(const Params& p, Smem* sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int t = warp; t < p.T; t += WARPS) select_token(p, sm, t, t % (int)gridDim.x == (int)blockIdx.x);
+  const int G = p.k + p.n_shared;
+  if (p.T <= SELECT_ALL_T) {
+    score_tokens(p, sm, 0, p.T);
+    __syncthreads();
+    if (warp < p.T) select_token(p, sm, warp, warp, warp % (int)gridDim.x == (int)blockIdx.x);
+    __syncthreads();
+  } else {
+    for (int t = (int)blockIdx.x; t < p.T; t += (int)gridDim.x) {
+      score_tokens(p, sm, t, 1);
+      __syncthreads();
+      if (warp == 0) select_token(p, sm, 0, t, true);
+      __syncthreads();
+    }
+    if (!grid_barrier(&p.bar[5], p, sm)) return false;
+    for (int i = tid; i < p.T * p.k; i += THREADS)
+      sm->pick[i / p.k * MOE_MAX_TOP_K + i % p.k] = (short)__ldcg(p.topk_idx + i);
+    for (int i = tid; i < p.T * G; i += THREADS) sm->gate[i / G * MAX_CONTRIB + i % G] = __ldcg(p.gates + i);
+    __syncthreads();
+  }
+  for (int i = tid; i < p.T * p.k; i += THREADS) {
+    const int t = i / p.k;
+    atomicOr(&sm->mask[sm->pick[t * MOE_MAX_TOP_K + i - t * p.k]], 1ull << t);
+  }
   __syncthreads();
   int n = 0, rows = 0, touched = 0;
   if (tid < MOE_MAX_ROUTED) {
@@ -603,7 +824,8 @@ __device__ __forceinline__ void route_all(const Params& p, Smem* sm) {
       rows += sm->warp_rows[w];
       touched += sm->warp_touched[w];
     }
-    sm->pre[tid] = rows - n;
+    sm->pre[tid] = (short)(rows - n);
+    sm->cnt[tid] = (short)n;
     if (n > 0) sm->list[touched - 1] = (short)tid;
     if (tid == MOE_MAX_ROUTED - 1) sm->n_touched = touched;
     if (blockIdx.x == 0 && tid < p.n_routed) p.counts[tid] = n;
@@ -615,171 +837,111 @@ __device__ __forceinline__ void route_all(const Params& p, Smem* sm) {
     const int row = sm->pre[e] + __popcll(sm->mask[e] & ((1ull << t) - 1ull));
     sm->row_of[t * MOE_MAX_TOP_K + q] = (short)row;
     sm->row_tok[row] = (uint8_t)t;
+    sm->row_exp[row] = (short)e;
   }
   __syncthreads();
-}
-
-// 8-bit experts, between the phases: each warp codes whole rows of h.
-__device__ __forceinline__ void code_hidden(const Params& p, int R) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int nv = p.f / 4;
-  for (int r = warp * (int)gridDim.x + (int)blockIdx.x; r < R; r += WARPS * (int)gridDim.x) {
-    const float4* row = reinterpret_cast<const float4*>(p.h) + (size_t)r * nv;
-    float m = 0.0f;
-    bool bad = false;
-    for (int i = lane; i < nv; i += 32) {
-      const float4 v = row[i];
-      const float a = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-      bad |= !(v.x - v.x == 0.0f) || !(v.y - v.y == 0.0f) || !(v.z - v.z == 0.0f) || !(v.w - v.w == 0.0f);
-      m = fmaxf(m, a);
-    }
-    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-    if (__any_sync(0xffffffffu, bad)) m = INFINITY;
-    const q8::RowScale rs = q8::row_scale(m);
-    for (int i = lane; i < nv; i += 32) {
-      const float4 v = row[i];
-      const float a[4] = {v.x, v.y, v.z, v.w};
-      reinterpret_cast<uint32_t*>(p.hq)[(size_t)r * nv + i] = q8::code4_f32(a, rs);
-    }
-    if (lane == 0) p.hs[r] = rs.scale;
-  }
+  return true;
 }
 
 template <bool I8>
-__global__ void __launch_bounds__(THREADS, 1) few_tokens_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, 1)
+    few_tokens_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,
+                      const Params p) {
   using T = typename AccT<I8>::type;
   extern __shared__ uint8_t smem_raw[];
-  Smem* sm = reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 15) & ~uintptr_t(15));
-  const int tid = threadIdx.x;
+  Smem* sm = reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int ELEM = I8 ? 1 : 2;
   const int f1 = p.swiglu ? 2 * p.f : p.f;
-  const Phase p1 = make_phase(p.w1, f1, p.d, ELEM, p.kw1, p.swiglu != 0, p.f);
-  const Phase p2 = make_phase(p.w2, p.d, p.f, ELEM, p.kw2, false, p.f);
 
   if (tid < MOE_MAX_ROUTED) sm->mask[tid] = 0;
-  if (tid == 0) sm->abort_flag = 0;
+  if (tid < WARPS) {
+    for (int i = 0; i < NST; ++i) mbar_init(&sm->ring_full[tid][i], 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) {
+    sm->abort_flag = 0;
+    sm->ph[0] = make_phase(f1, p.d, ELEM, p.swiglu != 0, p.f, p.s_log[0]);
+    sm->ph[0].items = NO_ITEM;  // not known yet
+  }
+  if (tid == 32) {
+    sm->ph[1] = make_phase(p.d, p.f, ELEM, false, p.f, p.s_log[1]);
+    tma_prefetch_desc(&tm1);
+    tma_prefetch_desc(&tm2);
+  }
 
-  // the shared experts' first weights need no routing: their copies run behind phase 0
-  Stream st;
-  st.phase = 1;
-  st.u = p1.w0;
-  st.c = p1.wk;
-  st.stage = 0;
-  int issued = 0;
-  stream_settle(st, p1, p2, p.n_shared, false, p, sm);
-  for (; issued < AHEAD && st.ready; ++issued) stream_issue(st, p1, p2, p.n_shared, false, p, sm);
-
+  // phase 0
   if (I8) code_tokens(p, sm);
   router_partial(p, sm);
-  bool ok = grid_barrier(&p.bar[0], p, sm);
+  fence_proxy_async_smem();  // the ring's memory was the router's: TMA writes come after
+  grid_arrive(&p.bar[0]);
+  // the shared experts' weights need no routing: their items fill the ring behind the barrier
+  Stream st;
+  st.ticket = warp * (int)gridDim.x + (int)blockIdx.x;
+  st.next = NO_ITEM;
+  st.stage = st.issued = st.pushed = 0;
+  int known = (p.n_shared * sm->ph[0].units) << p.s_log[0];
+  if (lane == 0) {
+    stream_begin(st, known, p, sm);
+    while (st.issued < NST && st.ready) stream_issue(st, &tm1, &tm2, known, p, sm);
+  }
+  Taken tk{0, 0u, 0};
+  bool ok = grid_wait(&p.bar[0], p, sm);
   if (ok) {
-    route_all(p, sm);
+    ok = route_all(p, sm);
+  }
+  if (ok) {
     const int n_exp = p.n_shared + sm->n_touched;
-    if (!st.ready) stream_settle(st, p1, p2, n_exp, true, p, sm);
-    for (; issued < AHEAD; ++issued) stream_issue(st, p1, p2, n_exp, true, p, sm);
-    auto next = [&]() { stream_issue(st, p1, p2, n_exp, true, p, sm); };
-    int stage = 0;
+    if (tid < 2) sm->ph[tid].items = (n_exp * sm->ph[tid].units) << p.s_log[tid];
+    __syncthreads();
+    known = NO_ITEM;
+    if (lane == 0) {
+      if (!st.ready) stream_begin(st, known, p, sm);
+      while (st.issued < NST && st.ready) stream_issue(st, &tm1, &tm2, known, p, sm);
+    }
+    auto next = [&]() { stream_issue(st, &tm1, &tm2, known, p, sm); };
     const int R = p.T * (p.k + p.n_shared);
 
-    // phase 1: hidden rows
-    for (int u = p1.w0; u < n_exp * p1.units; u += p1.stride) {
-      const int j = u / p1.units, b = u - j * p1.units;
-      const int e = expert_at(p, sm, j);
-      const bool shared = j < p.n_shared;
-      const int n_e = shared ? p.T : __popcll(sm->mask[e]);
-      const int row0 = shared ? p.T * p.k + j * p.T : sm->pre[e];
-      auto tok = [&](int col) { return shared ? col : (int)sm->row_tok[row0 + col]; };
-      auto put = [&](int col, int hc, float v) {
-        const size_t at = (size_t)(row0 + col) * p.f + hc;
-        if (I8) {
-          reinterpret_cast<float*>(p.h)[at] = v;
-        } else {
-          const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-          __nv_bfloat16* hp = reinterpret_cast<__nv_bfloat16*>(p.h);
-          hp[at] = hi;
-          // an infinite or NaN high part has no low part
-          const float lo = v - __bfloat162float(hi);
-          hp[at + (size_t)R * p.f] = __float2bfloat16_rn(lo - lo == 0.0f ? lo : 0.0f);
-        }
-      };
-      auto epi = [&](int col, int r, T a, T c) {
-        float va = (float)a, vc = (float)c;
-        const int ra = b * p1.row_mul + r;  // weight row of a; c's is 8 on, or the up row
-        if (I8) {
-          const float xs = __ldcg(p.xs + tok(col));
-          const float* ws = p.w1s + (size_t)e * f1;
-          va *= xs * __ldg(ws + ra);
-          vc *= xs * __ldg(ws + (p.swiglu ? p.f + ra : ra + 8));
-        }
-        if (p.swiglu) {
-          put(col, ra, silu_f32(va) * vc);
-        } else {
-          put(col, ra, gelu_tanh_exp_f32(va));
-          put(col, ra + 8, gelu_tanh_exp_f32(vc));
-        }
-      };
-      unit_any<T, 1>(p1, n_e, I8 ? p.xq : p.x, 0, tok, stage, sm, next, epi);
-    }
+    // phase 1
+    run_items<T, 0, 1>(p, I8 ? p.xq : p.x, 0, reinterpret_cast<T*>(p.u), f1, R, tk, sm, next);
     ok = grid_barrier(&p.bar[1], p, sm);
-    if (I8 && ok) {
-      code_hidden(p, R);
+    if (ok) {
+      if (I8)
+        code_hidden(p, sm, R);
+      else
+        finish_hidden(p, R);
       ok = grid_barrier(&p.bar[2], p, sm);
     }
-
-    // phase 2: expert outputs, and the sum over the experts of each completed block of columns
-    for (int u = p2.w0; ok && u < n_exp * p2.units; u += p2.stride) {
-      const int j = u / p2.units, b = u - j * p2.units;
-      const int e = expert_at(p, sm, j);
-      const bool shared = j < p.n_shared;
-      const int n_e = shared ? p.T : __popcll(sm->mask[e]);
-      const int row0 = shared ? p.T * p.k + j * p.T : sm->pre[e];
-      auto row = [&](int col) { return row0 + col; };
-      auto epi = [&](int col, int r, T a, T c) {
-        float va = (float)a, vc = (float)c;
-        const int ra = b * ROWS + r;
-        if (I8) {
-          const float hs = __ldcg(p.hs + row0 + col);
-          va *= hs * __ldg(p.w2s + (size_t)e * p.d + ra);
-          vc *= hs * __ldg(p.w2s + (size_t)e * p.d + ra + 8);
-        }
-        float* yr = p.y + (size_t)(row0 + col) * p.d + ra;
-        yr[0] = va;
-        yr[8] = vc;
-      };
-      unit_any<T, I8 ? 1 : 2>(p2, n_e, I8 ? p.hq : p.h, (size_t)R * p.f * 2, row, stage, sm, next, epi);
-      // unit() ended with the group's barrier: its stores are issued; the last expert to arrive adds up
-      const int group = (tid >> 5) / p2.kw, g_tid = p2.wk * 32 + (tid & 31);
-      if (g_tid == 0) {
-        __threadfence();
-        sm->flag[group] = atomicAdd(&p.blk_done[b], 1u) == (unsigned)(n_exp - 1);
-        __threadfence();
-      }
-      group_sync(group, p2.kw);
-      if (sm->flag[group]) {
-        for (int i = g_tid; i < p.T * ROWS; i += p2.kw * 32) {
-          const int t = i / ROWS, col = b * ROWS + i % ROWS;
-          float a = 0.0f;
-          for (int q = 0; q < p.k; ++q)
-            a = fmaf(sm->gate[t * MAX_CONTRIB + q],
-                     __ldcg(p.y + (size_t)sm->row_of[t * MOE_MAX_TOP_K + q] * p.d + col), a);
-          for (int q = 0; q < p.n_shared; ++q)
-            a = fmaf(sm->gate[t * MAX_CONTRIB + p.k + q],
-                     __ldcg(p.y + (size_t)(p.T * p.k + q * p.T + t) * p.d + col), a);
-          p.out[(size_t)t * p.d + col] = __float2bfloat16_rn(a);
-        }
-      }
-      group_sync(group, p2.kw);  // the flag is free again
+    // phase 2
+    if (ok) {
+      run_items<T, 1, I8 ? 1 : 2>(p, p.h, (size_t)R * p.f * 2, reinterpret_cast<T*>(p.y), p.d, R, tk, sm, next);
+      ok = grid_barrier(&p.bar[3], p, sm);
     }
+    if (ok) finish_out<I8>(p, sm, R);
   }
-  cp_async_wait<0>();
+  // nothing may still be landing in shared memory (only a call that ran out of time can have chunks left)
+  if (lane == 0) {
+    int zero = 0;
+    for (int i = max(0, st.issued - NST); i < st.issued; ++i)
+      mbar_wait(&sm->ring_full[warp][i % NST], (i / NST) & 1, p.timeout_ns, &zero, p.status);
+  }
 }
 
 // Scratch layout: byte offsets of each part.
 struct Layout {
-  size_t bar, blk, logits, xq, xs, h, hq, hs, y, bytes;
+  size_t bar, logits, xq, xs, u, h, hs, y, bytes;
+  int s_log[2];
 };
 
-inline Layout layout_of(int T, int d, int f, int n_shared, int k) {
+// log2 of the K slices of a matrix: enough items for a warp to take several (about six of 2368 warps), each at least
+// four boxes of K.
+inline int slices_log(double units, int nbox) {
+  int s = 0;
+  while ((1 << (s + 1)) <= S_MAX && (nbox >> (s + 1)) >= 4 && units * (1 << s) < 6.0 * 2368) ++s;
+  return s;
+}
+
+inline Layout layout_of(int T, int d, int f, int n_routed, int n_shared, int k, bool swiglu, int elem) {
   Layout l;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -787,26 +949,23 @@ inline Layout layout_of(int T, int d, int f, int n_shared, int k) {
     at += (bytes + 255) / 256 * 256;
     return here;
   };
+  // experts that T tokens touch when each picks k of n at random
+  double miss = 1.0;
+  for (int t = 0; t < T; ++t) miss *= 1.0 - (double)k / n_routed;
+  const double experts = n_shared + n_routed * (1.0 - miss);
+  l.s_log[0] = slices_log(experts * (f / (swiglu ? ROWS / 2 : ROWS)), (d * elem + BOX - 1) / BOX);
+  l.s_log[1] = slices_log(experts * (d / ROWS), (f * elem + BOX - 1) / BOX);
   const size_t R = (size_t)T * (k + n_shared);
-  l.bar = take(4 * sizeof(unsigned int));
-  l.blk = take((size_t)(d / ROWS) * sizeof(unsigned int));
+  l.bar = take(8 * sizeof(unsigned int));
   l.logits = take((size_t)KS_MAX * T * E_LD * sizeof(float));
   l.xq = take((size_t)T * d);
   l.xs = take((size_t)T * sizeof(float));
+  l.u = take((R * (swiglu ? 2 * f : f) * sizeof(float)) << l.s_log[0]);
   l.h = take(R * f * sizeof(float));
-  l.hq = take(R * f);
   l.hs = take(R * sizeof(float));
-  l.y = take(R * d * sizeof(float));
+  l.y = take((R * d * sizeof(float)) << l.s_log[1]);
   l.bytes = at;
   return l;
-}
-
-// Warps a row is split over: a power of two that leaves each warp at least four chunks, so the sum over the
-// warps at a unit's end stays small beside the unit.
-inline int split_for(int nch) {
-  int kw = 1;
-  while (kw < WARPS && nch / (2 * kw) >= 4) kw *= 2;
-  return kw;
 }
 
 template <bool I8>
@@ -828,7 +987,7 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
   if (T > MOE_FEW_MAX_T || n_routed > MOE_MAX_ROUTED || n_shared > MOE_MAX_SHARED) return MOE_ERR_UNSUPPORTED;
   if (d % 64 != 0 || d_ff % 64 != 0) return MOE_ERR_UNSUPPORTED;
   if (d > MOE_FEW_MAX_WIDTH || d_ff > MOE_FEW_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
-  const Layout l = layout_of(T, d, d_ff, n_shared, top_k);
+  const Layout l = layout_of(T, d, d_ff, n_routed, n_shared, top_k, activation == MOE_ACT_SWIGLU, I8 ? 1 : 2);
   if (scratch_bytes < l.bytes) return MOE_ERR_SCRATCH;
   cudaStream_t s = (cudaStream_t)stream;
   if (T == 0)
@@ -839,7 +998,7 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
   unsigned int* status = status_ptr();
   if (!status) return MOE_ERR_CUDA;
   auto kfn = few_tokens_kernel<I8>;
-  const size_t smem = sizeof(Smem) + 16;
+  const size_t smem = sizeof(Smem) + 1024;
   if ((rc = ensure_smem_attr((const void*)kfn, smem)) != MOE_OK) return rc;
 
   uint8_t* base = static_cast<uint8_t*>(scratch);
@@ -848,8 +1007,7 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
   p.w_r = reinterpret_cast<const uint8_t*>(w_router);
   p.bias = bias;
   p.offset = logit_offset;
-  p.w1 = static_cast<const uint8_t*>(w1);
-  p.w2 = static_cast<const uint8_t*>(w2);
+  p.elem = I8 ? 1 : 2;
   p.w1s = w1s;
   p.w2s = w2s;
   p.T = T;
@@ -865,26 +1023,32 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
   p.counts = counts;
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.bar = reinterpret_cast<unsigned int*>(base + l.bar);
-  p.blk_done = reinterpret_cast<unsigned int*>(base + l.blk);
   p.logits = reinterpret_cast<float*>(base + l.logits);
   p.xq = base + l.xq;
   p.xs = reinterpret_cast<float*>(base + l.xs);
+  p.u = reinterpret_cast<float*>(base + l.u);
   p.h = base + l.h;
-  p.hq = base + l.hq;
   p.hs = reinterpret_cast<float*>(base + l.hs);
   p.y = reinterpret_cast<float*>(base + l.y);
   p.timeout_ns = wait_timeout_ns();
   p.status = status;
-  const int elem = I8 ? 1 : 2;
-  p.kw1 = split_for((d * elem + CHUNK - 1) / CHUNK);
-  p.kw2 = split_for((d_ff * elem + CHUNK - 1) / CHUNK);
+  p.s_log[0] = l.s_log[0];
+  p.s_log[1] = l.s_log[1];
+  CUtensorMap tm1, tm2;
+  constexpr auto encode = I8 ? encode_tmap_u8 : encode_tmap_bf16;
+  const uint32_t box = BOX / p.elem, E = n_routed + n_shared;
+  if ((rc = encode(&tm1, w1, 3, d, p.swiglu ? 2 * d_ff : d_ff, E, box, p.swiglu ? ROWS / 2 : ROWS)) != MOE_OK)
+    return rc;
+  if ((rc = encode(&tm2, w2, 3, d_ff, d, E, box, ROWS)) != MOE_OK) return rc;
   const int rg_n = (n_routed + n_shared + ROWS - 1) / ROWS;
-  const int nch_r = (d * 2 + CHUNK - 1) / CHUNK;
-  p.ks = sms / rg_n;
-  p.ks = p.ks < 1 ? 1 : (p.ks > KS_MAX ? KS_MAX : p.ks);
-  if (p.ks > nch_r) p.ks = nch_r;
+  const int nch_r = (d * 2 + BOX - 1) / BOX;
+  // a chunk of K for every warp, in slices of as many CTAs as there are (every slice is read again by every
+  // CTA's selection, so no more than that)
+  p.ks = (nch_r + WARPS - 1) / WARPS;
+  if (p.ks > KS_MAX) p.ks = KS_MAX;
+  if (p.ks > sms / rg_n) p.ks = sms / rg_n > 1 ? sms / rg_n : 1;
 
-  // the barriers and block counters (adjacent at the start of the scratch) start at zero
+  // the barriers and the ticket counter start at zero
   if (cudaMemsetAsync(base + l.bar, 0, l.logits - l.bar, s) != cudaSuccess) return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms, 1, 1);
@@ -896,7 +1060,7 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kfn, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kfn, tm1, tm2, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MOE_ERR_CUDA;
   }
@@ -909,9 +1073,16 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
 using namespace moe;
 
 extern "C" size_t moe_few_tokens_scratch_bytes(int T, int d, int d_ff, int n_routed, int n_shared, int top_k) {
-  (void)n_routed;
-  if (T <= 0 || d <= 0 || d_ff <= 0 || n_shared < 0 || top_k < 1) return 256;
-  return few::layout_of(T, d, d_ff, n_shared, top_k).bytes;
+  if (T <= 0 || T > MOE_FEW_MAX_T || d <= 0 || d > MOE_FEW_MAX_WIDTH || d_ff <= 0 || d_ff > MOE_FEW_MAX_WIDTH ||
+      n_routed < 1 || n_shared < 0 || n_shared > MOE_MAX_SHARED || top_k < 1 || top_k > MOE_MAX_TOP_K)
+    return 256;
+  // what any form of the call with these sizes needs
+  size_t most = 0;
+  for (int form = 0; form < 4; ++form) {
+    const size_t b = few::layout_of(T, d, d_ff, n_routed, n_shared, top_k, (form & 1) != 0, 1 + (form >> 1)).bytes;
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 extern "C" int moe_few_tokens(const moe_bf16* x, const moe_bf16* w_router, const float* bias,
