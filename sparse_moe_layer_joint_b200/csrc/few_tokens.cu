@@ -15,7 +15,7 @@
 //             HBM's bandwidth do more of the work (with items dealt out in advance
 //             the first SM had read its share after 52 us and the last after 84).
 //   stream    Each warp has a ring of its own in shared memory (NST chunks of 256
-//             bytes of K by 16 rows, 192 KB an SM) that its lane 0 fills by TMA, so
+//             bytes of K by 16 rows, 128 KB an SM) that its lane 0 fills by TMA, so
 //             the stream needs no barrier, and runs on across items, from W1 into
 //             W2, and behind the grid barriers.  The loads are marked evict-first:
 //             a weight is read once, and L2 keeps what other kernels left there.
@@ -56,7 +56,7 @@ namespace few {
 
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
-constexpr int NST = 3;        // ring stages (chunks) per warp
+constexpr int NST = 2;        // ring stages (chunks) per warp
 constexpr int BOX = 128;      // bytes of K of one row a TMA box holds (one swizzle atom)
 constexpr int CHUNK = 256;    // and a chunk: two boxes side by side
 constexpr int STEPS = CHUNK / 64;  // 64-byte steps of K (two MMA instructions each)
@@ -933,11 +933,15 @@ struct Layout {
   int s_log[2];
 };
 
-// log2 of the K slices of a matrix: enough items for a warp to take several (about six of 2368 warps), each at least
-// four boxes of K.
+// log2 of the K slices of a matrix, for `units` blocks of 16 rows.  A phase ends when the last warp's last item does, so
+// an item should be short beside the phase: at least three items for each of 2368 warps, and as long as they are fewer
+// than sixteen each, at most 16 boxes of K (about 12 us).  Every item costs a ticket, its places and its partial sums,
+// so it keeps at least four boxes.  (32 tokens, SwiGLU, d 4096: items of 64 boxes left the first SM idle for 34 us.)
 inline int slices_log(double units, int nbox) {
   int s = 0;
-  while ((1 << (s + 1)) <= S_MAX && (nbox >> (s + 1)) >= 4 && units * (1 << s) < 6.0 * 2368) ++s;
+  while ((1 << (s + 1)) <= S_MAX && (nbox >> (s + 1)) >= 4 &&
+         (units * (1 << s) < 3.0 * 2368 || ((nbox >> s) > 16 && units * (1 << s) < 16.0 * 2368)))
+    ++s;
   return s;
 }
 
