@@ -149,7 +149,8 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building a Stream object costs a call more than its launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -280,16 +281,19 @@ def moe_nvfp4_grouped_gemm(aq, asf, offsets_pad, n_groups: int, rows_cap: int, w
 # ---------------------------------------------------------------------------
 # 8-bit experts (moe_int8_*) and the layer for a few tokens (moe_few_tokens*)
 # ---------------------------------------------------------------------------
-def _need(fn: str, dtype, *named):
-    """Check (name, tensor, elements) triples: contiguous CUDA tensors of ``dtype`` on the current device
-    with at least that many elements (None passes: the library decides which arguments may be null)."""
-    import torch
-
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for name, t, n in named:
-        if t is None or isinstance(t, int):
+def _need(fn: str, *named):
+    """Check (name, tensor, dtype, elements) of every tensor argument: contiguous, on the current CUDA device, with at
+    least that many elements (None and plain addresses pass: the library decides which arguments may be null)."""
+    cur = None
+    for name, t, dtype, n in named:
+        if t is None or t.__class__ is int:
             continue
-        if not t.is_cuda or t.get_device() != dev:
+        dev = t.get_device()
+        if cur is None and dev >= 0:
+            import torch
+
+            cur = torch.cuda.current_device()
+        if dev < 0 or dev != cur:
             raise ValueError(f"{fn}: {name} is on {t.device}, not on the current CUDA device")
         if t.dtype is not dtype:
             raise ValueError(f"{fn}: {name} is {t.dtype}, not {dtype}")
@@ -303,9 +307,7 @@ def moe_int8_quantize_rows(x, rows: int, K: int, q, scale, stream=None):
     import torch
 
     fn = "moe_int8_quantize_rows"
-    _need(fn, torch.bfloat16, ("x", x, rows * K))
-    _need(fn, torch.int8, ("q", q, rows * K))
-    _need(fn, torch.float32, ("scale", scale, rows))
+    _need(fn, ("x", x, torch.bfloat16, rows * K), ("q", q, torch.int8, rows * K), ("scale", scale, torch.float32, rows))
     _check(fn, _lib.moe_int8_quantize_rows(_p(x), rows, K, _p(q), _p(scale), _stream(stream)))
 
 
@@ -314,10 +316,9 @@ def moe_int8_dispatch(x, token_row, T: int, d: int, top_k: int, n_rows: int, xq,
     import torch
 
     fn = "moe_int8_dispatch"
-    _need(fn, torch.bfloat16, ("x", x, T * d))
-    _need(fn, torch.int32, ("token_row", token_row, T * top_k))
-    _need(fn, torch.int8, ("xq", xq, n_rows * d), ("xq_tok", xq_tok, T * d))
-    _need(fn, torch.float32, ("xs", xs, n_rows), ("xs_tok", xs_tok, T))
+    _need(fn, ("x", x, torch.bfloat16, T * d), ("token_row", token_row, torch.int32, T * top_k),
+          ("xq", xq, torch.int8, n_rows * d), ("xs", xs, torch.float32, n_rows),
+          ("xq_tok", xq_tok, torch.int8, T * d), ("xs_tok", xs_tok, torch.float32, T))
     _check(fn, _lib.moe_int8_dispatch(_p(x), _p(token_row), T, d, top_k, n_rows, _p(xq), _p(xs), _p(xq_tok),
                                       _p(xs_tok), _stream(stream)))
 
@@ -328,10 +329,10 @@ def moe_int8_grouped_gemm(aq, a_scale, offsets, n_groups: int, n_rows: int, expe
 
     fn = "moe_int8_grouped_gemm"
     w_rows = (expert_base + n_groups) * N * (2 if epilogue == MOE_INT8_EPI_SWIGLU else 1)
-    _need(fn, torch.int8, ("aq", aq, n_rows * K), ("wq", wq, w_rows * K))
-    _need(fn, torch.float32, ("a_scale", a_scale, n_rows), ("w_scale", w_scale, w_rows))
-    _need(fn, torch.int32, ("offsets", offsets, n_groups + 1))
-    _need(fn, torch.bfloat16, ("out", out, n_rows * N * (n_groups if offsets is None else 1)))
+    _need(fn, ("aq", aq, torch.int8, n_rows * K), ("a_scale", a_scale, torch.float32, n_rows),
+          ("offsets", offsets, torch.int32, n_groups + 1), ("wq", wq, torch.int8, w_rows * K),
+          ("w_scale", w_scale, torch.float32, w_rows),
+          ("out", out, torch.bfloat16, n_rows * N * (n_groups if offsets is None else 1)))
     _check(fn, _lib.moe_int8_grouped_gemm(_p(aq), _p(a_scale), _p(offsets), n_groups, n_rows, expert_base, _p(wq),
                                           _p(w_scale), N, K, epilogue, _p(out), _stream(stream)))
 
@@ -340,18 +341,19 @@ def moe_few_tokens_scratch_bytes(T: int, d: int, d_ff: int, n_routed: int, n_sha
     return int(_lib.moe_few_tokens_scratch_bytes(T, d, d_ff, n_routed, n_shared, top_k))
 
 
-def _need_few(fn, w_dtype, x, w_router, bias, logit_offset, w1, w2, T, d, d_ff, n_routed, n_shared, top_k, activation,
-              topk_idx, gates, counts, out, scratch, scratch_bytes):
+def _need_few(fn, w_dtype, x, w_router, bias, logit_offset, w1, w1_scale, w2, w2_scale, T, d, d_ff, n_routed, n_shared,
+              top_k, activation, topk_idx, gates, counts, out, scratch, scratch_bytes):
     import torch
 
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     E = n_routed + n_shared
     f1 = 2 * d_ff if activation == MOE_ACT_SWIGLU else d_ff
-    _need(fn, torch.bfloat16, ("x", x, T * d), ("w_router", w_router, E * d), ("out", out, T * d))
-    _need(fn, w_dtype, ("w1", w1, E * f1 * d), ("w2", w2, E * d * d_ff))
-    _need(fn, torch.float32, ("bias", bias, n_routed), ("logit_offset", logit_offset, n_routed),
-          ("gates", gates, T * (top_k + n_shared)))
-    _need(fn, torch.int32, ("topk_idx", topk_idx, T * top_k), ("counts", counts, n_routed))
-    _need(fn, torch.uint8, ("scratch", scratch, scratch_bytes))
+    _need(fn, ("x", x, bf16, T * d), ("w_router", w_router, bf16, E * d), ("bias", bias, f32, n_routed),
+          ("logit_offset", logit_offset, f32, n_routed), ("w1", w1, w_dtype, E * f1 * d),
+          ("w1_scale", w1_scale, f32, E * f1), ("w2", w2, w_dtype, E * d * d_ff), ("w2_scale", w2_scale, f32, E * d),
+          ("topk_idx", topk_idx, i32, T * top_k), ("gates", gates, f32, T * (top_k + n_shared)),
+          ("counts", counts, i32, n_routed), ("out", out, bf16, T * d),
+          ("scratch", scratch, torch.uint8, scratch_bytes))
 
 
 def moe_few_tokens(x, w_router, bias, logit_offset, w1, w2, T: int, d: int, d_ff: int, n_routed: int, n_shared: int,
@@ -360,8 +362,8 @@ def moe_few_tokens(x, w_router, bias, logit_offset, w1, w2, T: int, d: int, d_ff
     import torch
 
     fn = "moe_few_tokens"
-    _need_few(fn, torch.bfloat16, x, w_router, bias, logit_offset, w1, w2, T, d, d_ff, n_routed, n_shared, top_k,
-              activation, topk_idx, gates, counts, out, scratch, scratch_bytes)
+    _need_few(fn, torch.bfloat16, x, w_router, bias, logit_offset, w1, None, w2, None, T, d, d_ff, n_routed, n_shared,
+              top_k, activation, topk_idx, gates, counts, out, scratch, scratch_bytes)
     _check(fn, _lib.moe_few_tokens(
         _p(x), _p(w_router), _p(bias), _p(logit_offset), _p(w1), _p(w2), T, d, d_ff, n_routed, n_shared, top_k,
         route_scale, activation, _p(topk_idx), _p(gates), _p(counts), _p(out), _p(scratch), scratch_bytes,
@@ -374,11 +376,8 @@ def moe_few_tokens_int8(x, w_router, bias, logit_offset, w1, w1_scale, w2, w2_sc
     import torch
 
     fn = "moe_few_tokens_int8"
-    _need_few(fn, torch.int8, x, w_router, bias, logit_offset, w1, w2, T, d, d_ff, n_routed, n_shared, top_k,
-              activation, topk_idx, gates, counts, out, scratch, scratch_bytes)
-    f1 = 2 * d_ff if activation == MOE_ACT_SWIGLU else d_ff
-    _need(fn, torch.float32, ("w1_scale", w1_scale, (n_routed + n_shared) * f1),
-          ("w2_scale", w2_scale, (n_routed + n_shared) * d))
+    _need_few(fn, torch.int8, x, w_router, bias, logit_offset, w1, w1_scale, w2, w2_scale, T, d, d_ff, n_routed,
+              n_shared, top_k, activation, topk_idx, gates, counts, out, scratch, scratch_bytes)
     _check(fn, _lib.moe_few_tokens_int8(
         _p(x), _p(w_router), _p(bias), _p(logit_offset), _p(w1), _p(w1_scale), _p(w2), _p(w2_scale), T, d, d_ff,
         n_routed, n_shared, top_k, route_scale, activation, _p(topk_idx), _p(gates), _p(counts), _p(out), _p(scratch),

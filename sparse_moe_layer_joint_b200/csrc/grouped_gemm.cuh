@@ -37,9 +37,12 @@ constexpr int SWIGLU_OUT = BN / 2;
 // 512-column accumulator fills TMEM, so there is one accumulator, read by eight epilogue warps (two
 // per TMEM lane quarter, one per column half) into packed bf16 registers; the next tile's MMAs start
 // once every warp holds its share, while the warps store it.
-template <bool PAIR, int ST, bool WIDE = false>
+// I8 (8-bit operands, single CTAs): eight epilogue warps, two per TMEM lane quarter, each with half of the tile's
+// output columns; the products take half as long as bf16 ones, so the epilogue has half the time.
+template <bool PAIR, int ST, bool WIDE = false, bool I8 = false>
 struct Cfg {
   static_assert(!WIDE || PAIR, "wide tiles are pair tiles");
+  static_assert(!I8 || !PAIR, "8-bit operands run on single CTAs");
   static constexpr int NH = WIDE ? 2 : 1;          // 256-column halves per tile
   static constexpr int TILE_N = BN * NH;           // output columns per tile
   static constexpr int TILE_M = PAIR ? 256 : 128;  // rows per tile (per pair, or per CTA)
@@ -51,7 +54,7 @@ struct Cfg {
   static constexpr int B_HALF_BYTES = B_HALF_ROWS * BK * 2;
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int EPI_WARPS = 4 * NH;
+  static constexpr int EPI_WARPS = I8 ? 8 : 4 * NH;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int ACC_BUFS = WIDE ? 1 : 2;   // accumulators of 256 * NH columns in TMEM
   static constexpr uint32_t TX_BYTES = (PAIR ? 2 : 1) * STAGE_BYTES;  // bytes landing on the (leader's) full barrier
@@ -107,7 +110,17 @@ struct GroupTables {
   int prefix[MOE_MAX_GROUPS + 1];  // prefix[g] = row tiles of groups < g
 };
 
-template <int ST>
+constexpr int I8_COLS = BN / 2;          // accumulator columns an epilogue warp of the 8-bit kernel drains
+constexpr int I8_STAGE_BYTES = 32 * 64;  // and its staging of 32 rows by 32 bf16 columns
+
+// What the epilogue warps of the 8-bit kernel keep in shared memory.
+struct NoEpi {};
+struct I8Epi {
+  alignas(16) float scales[8][I8_COLS];       // channel scales
+  alignas(16) uint8_t stage[8][I8_STAGE_BYTES];  // outputs on their way to whole-sector stores
+};
+
+template <int ST, class EPI_SMEM = NoEpi>
 struct SmemTail {
   uint64_t full[ST];
   uint64_t empty[ST];
@@ -117,11 +130,15 @@ struct SmemTail {
   uint32_t tmem_base;
   int abort_flag;
   GroupTables gt;
+  EPI_SMEM epi;
 };
 
-template <bool PAIR, int ST, bool WIDE = false>
+template <bool PAIR, int ST, bool WIDE, bool I8>
+using Tail = SmemTail<ST, std::conditional_t<I8, I8Epi, NoEpi>>;
+
+template <bool PAIR, int ST, bool WIDE, bool I8>
 constexpr size_t smem_bytes() {
-  return 1024 /* alignment slack */ + (size_t)ST * Cfg<PAIR, ST, WIDE>::STAGE_BYTES + sizeof(SmemTail<ST>);
+  return 1024 /* alignment slack */ + (size_t)ST * Cfg<PAIR, ST, WIDE>::STAGE_BYTES + sizeof(Tail<PAIR, ST, WIDE, I8>);
 }
 
 struct Group {
@@ -237,31 +254,117 @@ __device__ __forceinline__ void build_tables(const Params& p, GroupTables& gt, i
   __syncthreads();
 }
 
-// 8-bit sums to values: v[i] holds the int32 bits of one row's columns, whose channel scales are at ws;
-// u = (row scale * channel scale) * sum.
+// 8-bit sums to values: v[i] holds the int32 bits of one row's columns, whose channel scales are at ws (shared
+// memory); u = (row scale * channel scale) * sum.
 template <int N>
 __device__ __forceinline__ void apply_scales(float (&v)[N], float row_scale, const float* ws) {
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
-    const float4 w = __ldg(reinterpret_cast<const float4*>(ws + i));
+    const float4 w = *reinterpret_cast<const float4*>(ws + i);
     const float m[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[i + q] = __fmul_rn(row_scale * m[q], (float)__float_as_int(v[i + q]));
   }
 }
 
+// Epilogue warps of the 8-bit kernel.  A warp drains 32 rows by half of the tile's columns, 32 outputs of every row at a
+// time: scales and activation in registers, then through shared memory, so that a store writes whole 64-byte pieces of
+// eight rows (a lane's own row in 16-byte stores left half of each 32-byte sector to another store: 8192 tokens of
+// d_ff 768 -> d 2048 took 104 us).  The channel scales are fetched while the tile's products run.
+template <int EPI, class TailT>
+__device__ __forceinline__ void epilogue_i8(const Params& p, TailT* st, uint32_t tmem_base, int unit, int n_units,
+                                            int total_tiles, int G, int warp, int lane) {
+  constexpr bool GATED = EPI == EPI_SWIGLU;
+  constexpr int OUT = GATED ? SWIGLU_OUT : BN;  // a tile's output columns
+  constexpr int MINE = OUT / 2;                 // this warp's
+  const int quarter = warp & 3, half = (warp - 2) >> 2;
+  float* ws = st->epi.scales[warp - 2];
+  uint8_t* stage = st->epi.stage[warp - 2];
+  volatile int* abort_flag = &st->abort_flag;
+  int acc = 0;
+  uint32_t acc_phase = 0;
+  for (int tile = unit; tile < total_tiles; tile += n_units) {
+    const TileInfo ti = tile_info(tile, st->gt.prefix, G, p.n_tiles_n, p.n_major_rows);
+    const Group gr = group_info(p, st->gt, ti.g);
+    const int r0 = ti.m * 128 + quarter * 32;  // the warp's first row in its group
+    const int col0 = ti.nt * OUT + half * MINE;
+    __nv_bfloat16* c = (gr.c_sel ? p.C1 : p.C0) + (size_t)(gr.c_base + r0) * p.ldc + col0;
+    const int rows = min(32, min(gr.rows, (gr.c_sel ? p.c1_limit : p.c0_limit) - gr.c_base) - r0);  // rows to store
+    const float row_scale = lane < rows ? __ldg(p.a_scale + gr.a_base + r0 + lane) : 0.0f;
+    {
+      // ws[0 .. 127]: the scales of the accumulator columns drained; gated: 64 gate columns', then the up columns'
+      const int x = lane * 4, cc = col0 + (GATED ? x % MINE : x);
+      const float* src = p.b_scale + (size_t)ti.g * p.b_scale_ld + (GATED && x >= MINE ? p.b_up_row : 0);
+      const float4 w = cc < p.N ? __ldg(reinterpret_cast<const float4*>(src + cc)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      __syncwarp();  // every lane is done with the last tile's
+      *reinterpret_cast<float4*>(ws + x) = w;
+      __syncwarp();
+    }
+    if (!mbar_wait(&st->tfull[acc], acc_phase, p.timeout_ns, abort_flag, p.status)) break;
+    tc_fence_after();
+    const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN + half * MINE);
+#pragma unroll 1
+    for (int ch = 0; ch < MINE / 32; ++ch) {
+      if (col0 + ch * 32 >= p.N) break;  // same for the whole warp
+      float v[32];
+      tmem_ld32(taddr + ch * 32, v);
+      apply_scales(v, row_scale, ws + ch * 32);
+      uint32_t pk[16];
+      if constexpr (GATED) {
+        float u[32];
+        tmem_ld32(taddr + SWIGLU_OUT + ch * 32, u);
+        apply_scales(u, row_scale, ws + MINE + ch * 32);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          pk[i] = pack_bf16x2(silu_f32(v[2 * i]) * u[2 * i], silu_f32(v[2 * i + 1]) * u[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float a = v[2 * i], b = v[2 * i + 1];
+          if (EPI == EPI_GELU) {
+            a = gelu_tanh_exp_f32(a);
+            b = gelu_tanh_exp_f32(b);
+          }
+          pk[i] = pack_bf16x2(a, b);
+        }
+      }
+      // row r's 16-byte piece q lies at r * 64 + (q ^ (r / 2 % 4)) * 16: no bank conflict either way
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) =
+            make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2), q = lane & 3;
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((q ^ (r >> 1 & 3)) << 4));
+        if (r < rows) *reinterpret_cast<uint4*>(c + (size_t)r * p.ldc + ch * 32 + q * 8) = w;
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&st->tempty[acc]);
+    if (++acc == 2) {
+      acc = 0;
+      acc_phase ^= 1u;
+    }
+  }
+}
+
 // I8: the operands are 8-bit codes (kind::i8, exact int32 accumulators) with scales applied by the epilogue;
 // a stage holds the same bytes, 128 codes of K, and the same four MMA steps of 32 bytes.
 template <int EPI, bool PAIR, int ST, bool WIDE, bool I8 = false>
-__global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE, I8>::THREADS, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                         const __grid_constant__ CUtensorMap tmB, const Params p) {
-  using C = Cfg<PAIR, ST, WIDE>;
+  using C = Cfg<PAIR, ST, WIDE, I8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* smemA = smem;
   uint8_t* smemB = smem + C::STAGES * C::A_BYTES;
-  SmemTail<ST>* st = reinterpret_cast<SmemTail<ST>*>(smem + C::STAGES * C::STAGE_BYTES);
+  using TailT = Tail<PAIR, ST, WIDE, I8>;
+  TailT* st = reinterpret_cast<TailT*>(smem + C::STAGES * C::STAGE_BYTES);
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -424,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE>::THREADS, 1)
     if (lane == 0 && leader) {
       // one MMA per 256-column half
       constexpr uint32_t idesc_full = I8 ? make_idesc_i8(C::TILE_M, BN) : make_idesc_bf16(C::TILE_M, BN);
-      constexpr uint32_t idesc_half = I8 ? make_idesc_i8(C::TILE_M / 2, BN) : make_idesc_bf16(C::TILE_M / 2, BN);
+      constexpr uint32_t idesc_half = make_idesc_bf16(C::TILE_M / 2, BN);
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -455,17 +558,12 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE>::THREADS, 1)
             for (int h = 0; h < C::NH; ++h) {
               const uint64_t bd = make_desc_sw128(b_addr + h * C::B_HALF_BYTES + k * 32);
               const uint32_t more = (kb | k) != 0 ? 1u : 0u;
-              if (PAIR) {
-                if (I8)
-                  mma_i8_ss_pair(d_tmem + h * h_cols, ad, bd, idesc, more);
-                else
-                  mma_bf16_ss_pair(d_tmem + h * h_cols, ad, bd, idesc, more);
-              } else {
-                if (I8)
-                  mma_i8_ss(d_tmem + h * BN, ad, bd, idesc_full, more);
-                else
-                  mma_bf16_ss(d_tmem + h * BN, ad, bd, idesc_full, more);
-              }
+              if (PAIR)
+                mma_bf16_ss_pair(d_tmem + h * h_cols, ad, bd, idesc, more);
+              else if (I8)
+                mma_i8_ss(d_tmem + h * BN, ad, bd, idesc_full, more);
+              else
+                mma_bf16_ss(d_tmem + h * BN, ad, bd, idesc_full, more);
             }
           }
           if (PAIR)
@@ -495,6 +593,8 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE>::THREADS, 1)
         mma_commit(&st->drain);
       mbar_wait(&st->drain, 0, p.timeout_ns, &zero, p.status);
     }
+  } else if constexpr (I8) {
+    epilogue_i8<EPI>(p, st, tmem_base, unit, n_units, total_tiles, G, warp, lane);
   } else {
     // ================= epilogue (warps 2 .. 2 + EPI_WARPS - 1) =================
     const int quarter = warp & 3;  // TMEM lanes this warp may access
@@ -529,11 +629,6 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE>::THREADS, 1)
       __nv_bfloat16* cbase = gr.c_sel ? p.C1 : p.C0;
       const int climit = gr.c_sel ? p.c1_limit : p.c0_limit;
       const bool valid = (r < gr.rows) && (c_row < climit);
-      // 8-bit operands: this row's scale, and the channel scales of output column c (columns past N, which
-      // are not stored, read column 0's)
-      const float row_scale = I8 && valid ? __ldg(p.a_scale + gr.a_base + r) : 0.0f;
-      const float* ws = I8 ? p.b_scale + (size_t)ti.g * p.b_scale_ld : nullptr;
-      auto ws_at = [&](int c) { return ws + (c < p.N ? c : 0); };
       if (!mbar_wait(&st->tfull[acc], acc_phase, p.timeout_ns, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t taddr =
@@ -551,11 +646,6 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE>::THREADS, 1)
           float g[16], u[16];
           tmem_ld16(tbase + c16 * 16, g);
           tmem_ld16(tbase + BN + c16 * 16, u);
-          if constexpr (I8) {
-            const float* wc = ws_at(ti.nt * BN + half * SWIGLU_OUT + c16 * 16);
-            apply_scales(g, row_scale, wc);
-            apply_scales(u, row_scale, wc + p.b_up_row);
-          }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             pk[c16 * 8 + i] = pack_bf16x2(silu_f32(g[2 * i]) * u[2 * i], silu_f32(g[2 * i + 1]) * u[2 * i + 1]);
@@ -589,13 +679,12 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE>::THREADS, 1)
           for (int c16 = 0; c16 < 2 * NCH; ++c16) {  // 16 columns at a time (register pressure)
             float v[16];
             tmem_ld16(taddr + c16 * 16, v);
-            if constexpr (I8) apply_scales(v, row_scale, ws_at(col_base + c16 * 16));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float a = v[2 * i], b = v[2 * i + 1];
               if (EPI == EPI_GELU) {
-                a = I8 ? gelu_tanh_exp_f32(a) : gelu_tanh_f32(a);
-                b = I8 ? gelu_tanh_exp_f32(b) : gelu_tanh_f32(b);
+                a = gelu_tanh_f32(a);
+                b = gelu_tanh_f32(b);
               }
               pk[c16 * 8 + i] = pack_bf16x2(a, b);
             }
@@ -631,10 +720,6 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE>::THREADS, 1)
           float g[32], u[32];
           tmem_ld32(taddr + ch * 32, g);
           tmem_ld32(taddr + SWIGLU_OUT + ch * 32, u);
-          if constexpr (I8) {
-            apply_scales(g, row_scale, ws + col0);
-            apply_scales(u, row_scale, ws + p.b_up_row + col0);
-          }
           if (valid) {
             uint32_t pk[16];
 #pragma unroll
@@ -650,15 +735,14 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE>::THREADS, 1)
         if (col0 >= p.N) break;  // same for the whole warp
         float v[32];
         tmem_ld32(taddr + ch * 32, v);
-        if constexpr (I8) apply_scales(v, row_scale, ws + col0);
         if (valid) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float a = v[2 * i], b = v[2 * i + 1];
             if (EPI == EPI_GELU) {
-              a = I8 ? gelu_tanh_exp_f32(a) : gelu_tanh_f32(a);
-              b = I8 ? gelu_tanh_exp_f32(b) : gelu_tanh_f32(b);
+              a = gelu_tanh_f32(a);
+              b = gelu_tanh_f32(b);
             }
             pk[i] = pack_bf16x2(a, b);
           }
@@ -699,8 +783,8 @@ template <int EPI, bool PAIR, int ST, bool WIDE = false, bool I8 = false>
 int launch_one(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b, const Params& p, int grid,
                cudaStream_t stream) {
   auto kfn = grouped_gemm_kernel<EPI, PAIR, ST, WIDE, I8>;
-  constexpr size_t bytes = smem_bytes<PAIR, ST, WIDE>();
-  constexpr int NUM_THREADS = Cfg<PAIR, ST, WIDE>::THREADS;
+  constexpr size_t bytes = smem_bytes<PAIR, ST, WIDE, I8>();
+  constexpr int NUM_THREADS = Cfg<PAIR, ST, WIDE, I8>::THREADS;
   static_assert(bytes <= 232448, "shared memory per CTA");
   int rc = ensure_smem_attr((const void*)kfn, bytes);
   if (rc != MOE_OK) return rc;
@@ -774,9 +858,9 @@ inline int stages_for(bool pair, bool wide, int which, double flop) {
 }
 
 // Groups of at most this many row tiles run column-tile-major; MOE_GEMM_NMAJOR=<rows> overrides (0: all
-// row-tile-major).
-inline int n_major_rows_for() {
-  int r = 0;
+// row-tile-major).  8-bit products ask for 4: groups of two to four row tiles ran 1-3% faster (192 rows a group, K 7168,
+// N 2048: 879 against 891 us), groups of twelve 6% slower.
+inline int n_major_rows_for(int r = 0) {
   const char* env = getenv("MOE_GEMM_NMAJOR");
   if (env && env[0]) r = atoi(env);
   return r < 0 ? 0 : r;
@@ -833,7 +917,7 @@ int run_gemm(const GemmSpec& g, bool pair, int stages, int sms, long long tiles_
   // up) for SwiGLU
   const uint32_t b_box = (pair || EPI == EPI_SWIGLU) ? (uint32_t)Cfg<true, 4>::B_HALF_ROWS
                                                      : (uint32_t)Cfg<false, 4>::B_HALF_ROWS;
-  const bool wide = wide_for(pair, EPI);
+  const bool wide = !I8 && wide_for(pair, EPI);
   Params p = g.p;
   if (wide)  // 512 output columns a tile; SwiGLU: 256 outputs (256 gate + 256 up accumulator columns)
     p.n_tiles_n = EPI == EPI_SWIGLU ? (p.N + BN - 1) / BN
@@ -852,17 +936,24 @@ int run_gemm(const GemmSpec& g, bool pair, int stages, int sms, long long tiles_
   }
   if ((rc = encode(&b, g.b, 3, K, N, (uint64_t)(g.p.G_r + g.p.G_s), KE, b_box)) != MOE_OK) return rc;
   long long units = tiles_upper * p.n_tiles_n;
-  if (pair) {
-    long long pairs = units < sms / 2 ? units : sms / 2;
-    if (wide) {
-      if (stages == 3) return launch_one<EPI, true, 3, true, I8>(a0, a1, b, p, (int)(2 * pairs), s);
-      return launch_one<EPI, true, 4, true, I8>(a0, a1, b, p, (int)(2 * pairs), s);
+  if constexpr (I8) {
+    // single CTAs at every size: 128 x 256 tiles with two accumulators beat pair tiles, whose products end sooner but
+    // whose one accumulator makes them wait for the epilogue (1536 rows a group, K 7168, N 2048: 537 us against 589 on
+    // 256 x 512 pair tiles and 551 on 256 x 256; only a single group of 9472 rows with K 16384 ran 12% faster on pairs)
+    return launch_one<EPI, false, 4, false, true>(a0, a1, b, p, (int)(units < sms ? units : sms), s);
+  } else {
+    if (pair) {
+      long long pairs = units < sms / 2 ? units : sms / 2;
+      if (wide) {
+        if (stages == 3) return launch_one<EPI, true, 3, true>(a0, a1, b, p, (int)(2 * pairs), s);
+        return launch_one<EPI, true, 4, true>(a0, a1, b, p, (int)(2 * pairs), s);
+      }
+      if (stages == 6) return launch_one<EPI, true, 6, false>(a0, a1, b, p, (int)(2 * pairs), s);
+      if (stages == 5) return launch_one<EPI, true, 5, false>(a0, a1, b, p, (int)(2 * pairs), s);
+      return launch_one<EPI, true, 4, false>(a0, a1, b, p, (int)(2 * pairs), s);
     }
-    if (stages == 6) return launch_one<EPI, true, 6, false, I8>(a0, a1, b, p, (int)(2 * pairs), s);
-    if (stages == 5) return launch_one<EPI, true, 5, false, I8>(a0, a1, b, p, (int)(2 * pairs), s);
-    return launch_one<EPI, true, 4, false, I8>(a0, a1, b, p, (int)(2 * pairs), s);
+    return launch_one<EPI, false, 4>(a0, a1, b, p, (int)(units < sms ? units : sms), s);
   }
-  return launch_one<EPI, false, 4, false, I8>(a0, a1, b, p, (int)(units < sms ? units : sms), s);
 }
 
 // Pair launches with each group's last rows split off: the CTA pairs take every group's whole

@@ -4,8 +4,11 @@
 //
 // Bound: HBM, 2 bytes read and 1 (dispatch: top_k or top_k + 1) written a value.
 // A row is held in registers between its maximum and its codes (VEC 16-byte
-// vectors a thread, TPR threads a row), so it is read once; rows too long for
-// that are read a second time, from L2.
+// vectors a thread, TPR threads a row), so it is read once; rows of more than
+// 16384 values are read a second time, from L2.  A value costs one conversion, one
+// fma and three quarters of a byte permute (int8.cuh): 24570 rows of 2048 take 26.6
+// us (5.7 TB/s), the dispatch of 16384 tokens of 4096 to six experts 94 us (6.4
+// TB/s), one 2048 x 7168 matrix 12 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -16,9 +19,6 @@
 
 namespace moe {
 namespace q8 {
-
-constexpr int THREADS = 256;
-constexpr int VEC = 4;  // 16-byte vectors of a row a thread holds
 
 struct Params {
   const uint4* x;
@@ -34,96 +34,115 @@ struct Params {
   float* scale;
 };
 
+constexpr int MIN_THREADS = 128;
+
 // Maximum over the TPR threads that share a row (a power of two; whole warps above 32).
-template <int TPR>
+template <int TPR, int THREADS>
 __device__ __forceinline__ uint32_t row_max(uint32_t m, uint32_t* part) {
-  constexpr int W = TPR < 32 ? TPR : 32;
+  if (TPR >= 32) {
+    m = __reduce_max_sync(0xffffffffu, m);
+  } else {
 #pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = TPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
   if (TPR <= 32) return m;
-  const int warp = threadIdx.x >> 5;
   constexpr int WPR = TPR > 32 ? TPR / 32 : 1;
-  __syncthreads();  // the previous row's parts have been read
+  const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) part[warp] = m;
   __syncthreads();
   const int first = warp / WPR * WPR;
+#pragma unroll
   for (int i = 0; i < WPR; ++i) m = max(m, part[first + i]);
   return m;
 }
 
-template <int TPR, bool LONG>
+// TPR threads a row, each holding VEC of its 16-byte vectors; LONG: rows with more than TPR * VEC of them.
+template <int TPR, int VEC, bool LONG, int THREADS>
 __global__ void __launch_bounds__(THREADS) code_rows_kernel(const Params p) {
   __shared__ uint32_t part[THREADS / 32];
-  constexpr int RPB = THREADS / TPR;  // rows a block works on at once
   const int lane = threadIdx.x % TPR;
-  // every thread runs every iteration (the row maximum is a block-wide step)
-  for (long long r0 = (long long)blockIdx.x * RPB; r0 < p.rows; r0 += (long long)gridDim.x * RPB) {
-    const long long r = r0 + threadIdx.x / TPR;
-    const bool live = r < p.rows;
-    const uint4* row = p.x + r * p.nv;
-    uint4 v[VEC];
-    uint32_t m = 0;
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int c = lane + i * TPR;
-        v[i] = c < p.nv ? __ldg(row + c) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) m = max(m, abs_max_bits(v[i]));
-      if (LONG)
-        for (int c = lane + VEC * TPR; c < p.nv; c += TPR) m = max(m, abs_max_bits(__ldg(row + c)));
-    }
-    m = row_max<TPR>(m, part);
-    if (!live) continue;
-    const RowScale rs = row_scale(__uint_as_float(m << 16));
-    auto put = [&](int c, const uint4& src) {
-      const uint2 code = code8(src, rs);
-      if (p.q) p.q[r * p.nv + c] = code;
-      if (p.token_row)
-        for (int j = 0; j < p.k; ++j) {
-          const int to = __ldg(p.token_row + r * p.k + j);
-          if (to >= 0 && to < p.n_rows) p.xq[(long long)to * p.nv + c] = code;
-        }
-    };
+  const long long r = (long long)blockIdx.x * (THREADS / TPR) + threadIdx.x / TPR;
+  const bool live = r < p.rows;  // a dead row's threads still take part in the block's maximum
+  const uint4* row = p.x + r * p.nv;
+  uint4 v[VEC];
+  uint32_t m = 0;
+  if (live) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const int c = lane + i * TPR;
-      if (c < p.nv) put(c, v[i]);
+      v[i] = c < p.nv ? __ldg(row + c) : make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) m = max(m, abs_max_bits(v[i]));
     if (LONG)
-      for (int c = lane + VEC * TPR; c < p.nv; c += TPR) put(c, __ldg(row + c));
-    if (lane == 0) {
-      if (p.scale) p.scale[r] = rs.scale;
-      if (p.token_row)
-        for (int j = 0; j < p.k; ++j) {
-          const int to = __ldg(p.token_row + r * p.k + j);
-          if (to >= 0 && to < p.n_rows) p.xs[to] = rs.scale;
-        }
+      for (int c = lane + VEC * TPR; c < p.nv; c += TPR) m = max(m, abs_max_bits(__ldg(row + c)));
+  }
+  m = row_max<TPR, THREADS>(m, part);
+  if (!live) return;
+  const RowScale rs = row_scale(__uint_as_float(m << 16));
+  // the row's copies: its place in token order, and the rows its experts take
+  long long to[MOE_MAX_TOP_K];
+#pragma unroll
+  for (int j = 0; j < MOE_MAX_TOP_K; ++j) {
+    to[j] = -1;
+    if (p.token_row && j < p.k) {
+      const int t = __ldg(p.token_row + r * p.k + j);
+      if (t >= 0 && t < p.n_rows) to[j] = t;
     }
+  }
+  auto put = [&](int c, const uint4& src) {
+    const uint2 code = code8(src, rs);
+    if (p.q) p.q[r * p.nv + c] = code;
+    if (p.token_row) {
+#pragma unroll
+      for (int j = 0; j < MOE_MAX_TOP_K; ++j)
+        if (to[j] >= 0) p.xq[to[j] * p.nv + c] = code;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const int c = lane + i * TPR;
+    if (c < p.nv) put(c, v[i]);
+  }
+  if (LONG)
+    for (int c = lane + VEC * TPR; c < p.nv; c += TPR) put(c, __ldg(row + c));
+  if (lane == 0) {
+    if (p.scale) p.scale[r] = rs.scale;
+#pragma unroll
+    for (int j = 0; j < MOE_MAX_TOP_K; ++j)
+      if (to[j] >= 0) p.xs[to[j]] = rs.scale;
   }
 }
 
-template <int TPR, bool LONG>
-int launch(const Params& p, int sms, cudaStream_t s) {
-  constexpr int RPB = THREADS / TPR;
-  const long long want = (p.rows + RPB - 1) / RPB;
-  const long long most = (long long)sms * 8;
-  code_rows_kernel<TPR, LONG><<<(int)(want < most ? want : most), THREADS, 0, s>>>(p);
+template <int TPR, int VEC, bool LONG = false>
+int launch(const Params& p, cudaStream_t s) {
+  constexpr int THREADS = TPR > MIN_THREADS ? TPR : MIN_THREADS;
+  const long long blocks = (p.rows + THREADS / TPR - 1) / (THREADS / TPR);
+  if (blocks > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  code_rows_kernel<TPR, VEC, LONG, THREADS><<<(int)blocks, THREADS, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// Threads a row: the fewest (of 8 to 256) whose VEC vectors hold the whole row.
+// Threads a row.  Many rows: 16 vectors a thread, so that few threads hold a row's loads in flight and short blocks
+// replace each other (30000 rows of 7168: 98 us at 64 threads, 111 at 128, 123 at 256).  Few rows, where latency counts,
+// and the dispatch, whose stores outweigh its loads: 8 vectors (one token of 4096, top-6: 6.1 against 8.2 us; 16384 tokens:
+// 94 against 97).
 int run(const Params& p, cudaStream_t s) {
-  int dev, sms;
-  const int rc = device_info(&dev, &sms);
-  if (rc != MOE_OK) return rc;
-  if (p.nv <= 8 * VEC) return launch<8, false>(p, sms, s);
-  if (p.nv <= 32 * VEC) return launch<32, false>(p, sms, s);
-  if (p.nv <= 64 * VEC) return launch<64, false>(p, sms, s);
-  if (p.nv <= 128 * VEC) return launch<128, false>(p, sms, s);
-  if (p.nv <= 256 * VEC) return launch<256, false>(p, sms, s);
-  return launch<256, true>(p, sms, s);
+  if (p.nv > 2048) return launch<512, 8, true>(p, s);
+  if (p.nv <= 32) return launch<8, 4>(p, s);
+  if (p.rows <= 1024 || p.token_row) {
+    if (p.nv <= 128) return launch<32, 4>(p, s);
+    if (p.nv <= 256) return launch<32, 8>(p, s);
+    if (p.nv <= 512) return launch<64, 8>(p, s);
+    if (p.nv <= 1024) return launch<128, 8>(p, s);
+    return launch<256, 8>(p, s);
+  }
+  if (p.nv <= 64) return launch<16, 4>(p, s);
+  if (p.nv <= 128) return launch<16, 8>(p, s);
+  if (p.nv <= 256) return launch<32, 8>(p, s);
+  if (p.nv <= 512) return launch<32, 16>(p, s);
+  if (p.nv <= 1024) return launch<64, 16>(p, s);
+  return launch<128, 16>(p, s);
 }
 
 }  // namespace q8

@@ -11,19 +11,21 @@ namespace moe {
 namespace q8 {
 
 struct RowScale {
-  float pre;    // power of two that lifts tiny rows into fp32's normal range
-  float inv;    // 127 / (a * pre)
+  float inv;    // 127 / (a * pre), rounded up
   float scale;  // a / 127
+  bool tiny;    // the row is lifted by `pre` = 2^66 so that inv does not overflow
   bool zero;    // every code is 0
 };
+
+constexpr float TINY_PRE = 0x1p66f;
 
 __device__ __forceinline__ RowScale row_scale(float a) {
   RowScale r;
   const bool finite = a < INFINITY;  // false for NaN too
   r.zero = !finite || a == 0.0f;
   r.scale = finite ? __fdiv_rn(a, 127.0f) : __uint_as_float(0x7fffffffu);
-  r.pre = a < 0x1p-60f ? 0x1p66f : 1.0f;
-  r.inv = r.zero ? 0.0f : __fdiv_rn(127.0f, a * r.pre);
+  r.tiny = a < 0x1p-60f;
+  r.inv = r.zero ? 0.0f : __fdiv_ru(127.0f, r.tiny ? a * TINY_PRE : a);
   return r;
 }
 
@@ -35,42 +37,51 @@ __device__ __forceinline__ uint32_t abs_max_bits(const uint4& v) {
   return max(m & 0xffffu, m >> 16);
 }
 
-// Adding 1.5 * 2^23 rounds |q| <= 127 to the nearest integer, ties to even, and leaves its two's complement
-// in the low byte.
-__device__ __forceinline__ uint32_t to_code(float q) { return __float_as_uint(__fadd_rn(q, 12582912.0f)); }
+// The code of v in the low byte: v * inv rounded once to the nearest integer, ties to even, by adding 1.5 * 2^23 in the
+// same fma (the sum's low byte is the integer's two's complement).
+//
+// For bf16 values this is the exact code of 127 v / a.  With 8-bit significands A of a and X of |v|, a half-integer
+// quotient o / 2 means 254 X = o A 2^m, so the prime 127 divides A or o.  If it divides A, 127 / a is a power of two and
+// inv and the product are exact.  If it divides o <= 253, then o = 127, |v| = a / 2, and inv rounded up makes the product
+// 63.5 or just above: 64, the even neighbour, either way.  Every other quotient is at least 1.5e-5 of its value away
+// from a half-integer, and inv is within 1.2e-7 of 127 / a.
+__device__ __forceinline__ uint32_t to_code(float v, float inv) { return __float_as_uint(__fmaf_rn(v, inv, 12582912.0f)); }
 
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// The exact code of a bf16 value without a division.  With 8-bit significands, 127 v / a is either exactly a
-// half-integer or at least 1.5e-5 of its value away from one, and q = fl(v * fl(127 / a)) is within 2.4e-7 of
-// it.  Rounding q to 17 significant bits (Veltkamp's splitting, within 3.9e-6) therefore lands on a
-// half-integer exactly when the quotient is one, so the final rounding to even decides true ties only.
-__device__ __forceinline__ uint32_t code_bf16(float v, const RowScale& r) {
-  const float q = __fmul_rn(__fmul_rn(v, r.pre), r.inv);
-  const float c = __fmul_rn(q, 129.0f);
-  return to_code(__fsub_rn(c, __fsub_rn(c, q)));
+template <int N>
+__device__ __forceinline__ void code_n(const float (&v)[N], const RowScale& r, uint32_t (&c)[N]) {
+  if (r.tiny) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = to_code(v[i] * TINY_PRE, r.inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = to_code(v[i], r.inv);
+  }
 }
 
+// Codes of eight packed bf16 values.
 __device__ __forceinline__ uint2 code8(const uint4& v, const RowScale& r) {
   if (r.zero) return make_uint2(0, 0);
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t c[8];
+  float f[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    c[2 * i] = code_bf16(__uint_as_float(w[i] << 16), r);
-    c[2 * i + 1] = code_bf16(__uint_as_float(w[i] & 0xffff0000u), r);
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+  uint32_t c[8];
+  code_n(f, r, c);
   return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
 }
 
-// Codes of four fp32 values (within 2.4e-7 of the quotient before the rounding to an integer).
+// Codes of four fp32 values.
 __device__ __forceinline__ uint32_t code4_f32(const float (&v)[4], const RowScale& r) {
   if (r.zero) return 0;
   uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = to_code(__fmul_rn(__fmul_rn(v[i], r.pre), r.inv));
+  code_n(v, r, c);
   return pack4(c[0], c[1], c[2], c[3]);
 }
 

@@ -38,10 +38,9 @@ extern "C" int moe_int8_grouped_gemm(const int8_t* aq, const float* a_scale, con
 
   const bool swiglu = epilogue == MOE_INT8_EPI_SWIGLU;
   const int w_rows = swiglu ? 2 * N : N;
-  const bool pair = choose_pair(out_rows, n_groups);
-  const int tile_m = pair ? Cfg<true, 4>::TILE_M : Cfg<false, 4>::TILE_M;
-  const long long tiles_upper = identity ? (long long)n_groups * ((n_rows + tile_m - 1) / tile_m)
-                                         : (n_rows + tile_m - 1) / tile_m + n_groups;
+  constexpr int TILE_M = Cfg<false, 4, false, true>::TILE_M;
+  const long long tiles_upper = identity ? (long long)n_groups * ((n_rows + TILE_M - 1) / TILE_M)
+                                         : (n_rows + TILE_M - 1) / TILE_M + n_groups;
 
   GemmSpec g{};
   g.a0 = aq;
@@ -56,9 +55,7 @@ extern "C" int moe_int8_grouped_gemm(const int8_t* aq, const float* a_scale, con
   p.shared_rows = n_rows;
   p.timeout_ns = wait_timeout_ns();
   p.status = status;
-  p.hints = hints_for();
-  p.n_major_rows = n_major_rows_for();
-  p.prefetch_kb = prefetch_for();
+  p.n_major_rows = n_major_rows_for(4);
   p.a_scale = a_scale;
   p.b_scale = w_scale + (size_t)expert_base * w_rows;
   p.b_scale_ld = w_rows;
@@ -70,18 +67,9 @@ extern "C" int moe_int8_grouped_gemm(const int8_t* aq, const float* a_scale, con
   p.n_tiles_n = swiglu ? (N + SWIGLU_OUT - 1) / SWIGLU_OUT : (N + BN - 1) / BN;
   p.b_up_row = N;
   p.ldc = N;
-  // the tensor cores do 8-bit work at twice the bf16 rate, so a launch of as many operations is half as long
-  const double flop = (double)out_rows * K * w_rows;
-  const int which = epilogue == MOE_INT8_EPI_BF16 ? 2 : 1;
   switch (epilogue) {
-    case MOE_INT8_EPI_BF16:
-      return run_gemm<EPI_NONE, true>(g, pair, stages_for(pair, wide_for(pair, EPI_NONE), which, flop), sms,
-                                      tiles_upper, s);
-    case MOE_INT8_EPI_GELU:
-      return run_gemm<EPI_GELU, true>(g, pair, stages_for(pair, wide_for(pair, EPI_GELU), which, flop), sms,
-                                      tiles_upper, s);
-    default:
-      return run_gemm<EPI_SWIGLU, true>(g, pair, stages_for(pair, wide_for(pair, EPI_SWIGLU), which, flop), sms,
-                                        tiles_upper, s);
+    case MOE_INT8_EPI_BF16: return run_gemm<EPI_NONE, true>(g, false, 4, sms, tiles_upper, s);
+    case MOE_INT8_EPI_GELU: return run_gemm<EPI_GELU, true>(g, false, 4, sms, tiles_upper, s);
+    default: return run_gemm<EPI_SWIGLU, true>(g, false, 4, sms, tiles_upper, s);
   }
 }
