@@ -167,6 +167,25 @@ int encode_tmap_u8_plain(CUtensorMap* map, const void* base, uint64_t dim0, uint
   return encode_tmap(map, base, 1, 2, dim0, dim1, 1, box0, box1, false);
 }
 
+int encode_tmap_5d(CUtensorMap* map, const void* base, int elem_bytes, const uint64_t dims[5],
+                   const uint64_t strides[4], const uint32_t box[5]) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return MOE_ERR_CUDA;
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], estr[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < 5; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    if (i < 4) st[i] = strides[i];
+  }
+  memset(map, 0, sizeof(*map));
+  const CUresult r =
+      fn(map, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 5,
+         const_cast<void*>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
 namespace {
 
 // One thread waits on a barrier that expects two arrivals but gets one.

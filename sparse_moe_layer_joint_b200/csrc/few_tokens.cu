@@ -81,7 +81,7 @@ struct Params {
   const float* offset;
   const float* w1s;  // [E, f1] channel scales (int8)
   const float* w2s;  // [E, d]
-  int elem;          // bytes of an expert weight
+  int plain_map[2];  // W1's / W2's rows are not whole boxes: the map has three dimensions
   int T, d, f, n_routed, n_shared, k;
   int swiglu;
   float gate_scale;
@@ -108,7 +108,7 @@ struct Params {
 // expert, t / S = j * units + b.
 struct Phase {
   int k_bytes;  // bytes of a row
-  int nbox;     // boxes of a row
+  int nch;      // chunks of a row
   int units;    // blocks of 16 rows per expert
   int s_log;
   int row_mul;  // first row of block b: b * row_mul
@@ -218,7 +218,7 @@ __device__ __forceinline__ uint4 load16(const uint8_t* p) { return *reinterpret_
 __device__ __forceinline__ Phase make_phase(int rows, int K, int elem, bool gated, int f, int s_log) {
   Phase ph;
   ph.k_bytes = K * elem;
-  ph.nbox = (ph.k_bytes + BOX - 1) / BOX;
+  ph.nch = (ph.k_bytes + CHUNK - 1) / CHUNK;
   ph.units = gated ? f / (ROWS / 2) : rows / ROWS;
   ph.s_log = s_log;
   ph.row_mul = gated ? ROWS / 2 : ROWS;
@@ -227,7 +227,7 @@ __device__ __forceinline__ Phase make_phase(int rows, int K, int elem, bool gate
   return ph;
 }
 
-// An item: slice s (boxes lo .. hi - 1) of block b of the j-th expert.
+// An item: slice s (chunks lo .. hi - 1) of block b of the j-th expert.
 struct Item {
   int j, b, s, lo, hi;
 };
@@ -238,8 +238,8 @@ __device__ __forceinline__ Item item_at(const Phase& ph, int t) {
   const int u = t >> ph.s_log;
   it.j = u / ph.units;
   it.b = u - it.j * ph.units;
-  it.lo = (ph.nbox * it.s) >> ph.s_log;
-  it.hi = (ph.nbox * (it.s + 1)) >> ph.s_log;
+  it.lo = (ph.nch * it.s) >> ph.s_log;
+  it.hi = (ph.nch * (it.s + 1)) >> ph.s_log;
   return it;
 }
 
@@ -247,11 +247,12 @@ __device__ __forceinline__ int expert_at(const Params& p, const Smem* sm, int j)
   return j < p.n_shared ? p.n_routed + j : sm->list[j - p.n_shared];
 }
 
-// The warp's weight stream, kept by its lane 0: item by item, two boxes of K at a time.
+// The warp's weight stream, kept by its lane 0: item by item, a chunk at a time.
 struct Stream {
-  int ticket, next;  // the item being loaded (or held), the one drawn for after it
+  int ticket;        // the item being loaded (or held)
+  unsigned int next; // the draw for the item after it, as the counter returned it: nothing may use it before it is needed
   int phase;
-  int box, hi;       // next box of the item, its end
+  int ch, hi;        // next chunk of the item, its end
   int row, e;        // the item's first row, and expert
   int stage, issued, pushed;
   bool ready;        // the item's place is known
@@ -270,35 +271,39 @@ __device__ __forceinline__ void stream_begin(Stream& s, int known, const Params&
   sm->queue[warp][s.pushed++ & (QUEUE - 1)] = any ? s.ticket : NO_ITEM;
   if (!any) return;
   const Item it = item_at(ph, t);
-  s.box = it.lo;
+  s.ch = it.lo;
   s.hi = it.hi;
   s.row = it.b * ph.row_mul;
   s.e = expert_at(p, sm, it.j);
   s.ready = true;
-  s.next = (int)(atomicAdd(p.bar + 4, 1u) + gridDim.x * WARPS);  // every warp's first item is its own number
+  s.next = atomicAdd(p.bar + 4, 1u);
 }
 
-// Load the next chunk into the next stage, which the warp has read.
+// Load the next chunk into the next stage, which the warp has read.  The matrices' maps have K as blocks of 128 bytes
+// next to each other in a dimension of their own, and the gate and up rows likewise, so that one load brings the whole
+// chunk; rows that are not whole blocks (8-bit, K an odd multiple of 64) take a plain map and a load a box.
 __device__ __forceinline__ void stream_issue(Stream& s, const CUtensorMap* tm1, const CUtensorMap* tm2, int known,
-                                             const Params& p, Smem* sm) {
-  if (!s.ready || *(volatile int*)&sm->abort_flag) return;
+                                             uint64_t pol, const Params& p, Smem* sm) {
+  if (!s.ready) return;
   const CUtensorMap* map = s.phase == 0 ? tm1 : tm2;
-  const int warp = threadIdx.x >> 5, up_row = sm->ph[s.phase].up_row;
+  const int warp = threadIdx.x >> 5;
   uint8_t* dst = sm->ring[warp][s.stage];
   uint64_t* bar = &sm->ring_full[warp][s.stage];
-  const int n = min(CHUNK / BOX, s.hi - s.box);
-  const uint64_t pol = l2_policy_evict_first();
-  mbar_arrive_expect_tx(bar, n * BOX_BYTES);
-  for (int h = 0; h < n; ++h) {  // K past the row's end reads zeros
-    const int x = (s.box + h) * BOX >> (p.elem - 1);
-    tma_load_3d_hint(dst + h * BOX_BYTES, map, bar, x, s.row, s.e, pol);
-    if (up_row != 0) tma_load_3d_hint(dst + h * BOX_BYTES + BOX_BYTES / 2, map, bar, x, s.row + up_row, s.e, pol);
+  mbar_arrive_expect_tx(bar, STAGE_BYTES);  // what lies past the row's end arrives as zeros
+  if (!p.plain_map[s.phase]) {
+    tma_load_5d_hint(dst, map, bar, 0, s.row, 0, s.ch * (CHUNK / BOX), s.e, pol);
+  } else {
+    const int up_row = sm->ph[s.phase].up_row;
+    for (int h = 0; h < CHUNK / BOX; ++h) {
+      const int x = s.ch * CHUNK + h * BOX;
+      tma_load_3d_hint(dst + h * BOX_BYTES, map, bar, x, s.row, s.e, pol);
+      if (up_row != 0) tma_load_3d_hint(dst + h * BOX_BYTES + BOX_BYTES / 2, map, bar, x, s.row + up_row, s.e, pol);
+    }
   }
   ++s.issued;
   s.stage = s.stage + 1 == NST ? 0 : s.stage + 1;
-  s.box += n;
-  if (s.box >= s.hi) {
-    s.ticket = s.next;
+  if (++s.ch >= s.hi) {
+    s.ticket = (int)(s.next + gridDim.x * WARPS);  // every warp's first item is its own number
     stream_begin(s, known, p, sm);
   }
 }
@@ -311,7 +316,7 @@ struct Taken {
   int head;
 };
 
-// An item's products: its boxes of 16 weight rows against the expert's n_e token rows, NT tiles of 8.
+// An item's products: its chunks of 16 weight rows against the expert's n_e token rows, NT tiles of 8.
 // b_base + row_of_col(col) * k_bytes is a token row; PARTS > 1: further parts b_part bytes apart.  False when
 // the call has run out of time.
 template <class T, int NT, int PARTS, class RowFn, class NextFn>
@@ -321,43 +326,54 @@ __device__ __forceinline__ bool item_products(T (&acc)[NT][4], int k_bytes, cons
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, c4 = lane & 3;
   // 16-byte piece q of row r lies at piece q ^ (r % 8) of the row's 128 bytes
-  const int at0 = r * BOX + ((c4 ^ r) << 4), at1 = r * BOX + (((c4 + 4) ^ r) << 4);
-  constexpr uint32_t NONE = 0xffffffffu;
-  uint32_t bp[NT];  // the lane's token rows as offsets (at most 64 MB)
+  const uint8_t* ring = sm->ring[warp][0] + r * BOX;
+  const int at0 = (c4 ^ r) << 4, at1 = ((c4 + 4) ^ r) << 4;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint8_t* bp[NT];  // the lane's token rows
+  constexpr bool EARLY = NT * PARTS <= 2;  // few enough to hold: the token loads go out before the wait
+  uint4 b[EARLY ? NT * PARTS : 1][STEPS];  // (columns without a token stay zero)
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int col = j * 8 + r;
-    bp[j] = col < n_e ? (uint32_t)row_of_col(col) * (uint32_t)k_bytes + c4 * 16 : NONE;
+    bp[j] = col < n_e ? b_base + (size_t)row_of_col(col) * k_bytes + it.lo * CHUNK + c4 * 16 : nullptr;
     acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0;
   }
-  constexpr bool EARLY = NT * PARTS <= 2;  // few enough to hold: the token loads go out before the wait
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int box = it.lo; box < it.hi; box += CHUNK / BOX) {
-    const int off = box * BOX, end = min(k_bytes, it.hi * BOX);
-    // a token's 16 bytes of step i; zeros past the slice, where the stage holds an older chunk's weights
-    auto token = [&](int j, int q, int i) {
-      return bp[j] != NONE && off + i * 64 < end ? load16(b_base + q * b_part + (bp[j] + off + i * 64)) : zero;
-    };
-    uint4 b[EARLY ? NT * PARTS : 1][STEPS];
+  if (EARLY) {
+#pragma unroll
+    for (int x = 0; x < NT * PARTS; ++x)
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) b[x][i] = zero;
+  }
+  for (int ch = it.lo; ch < it.hi; ++ch) {
+    const int left = k_bytes - ch * CHUNK;  // bytes of the row from here on
     if (EARLY) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
+        if (bp[j]) {
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q)
+          for (int q = 0; q < PARTS; ++q) {
+            const uint8_t* src = bp[j] + q * b_part;
+            if (left >= CHUNK) {
 #pragma unroll
-          for (int i = 0; i < STEPS; ++i) b[j * PARTS + q][i] = token(j, q, i);
+              for (int i = 0; i < STEPS; ++i) b[j * PARTS + q][i] = load16(src + i * 64);
+            } else {
+#pragma unroll
+              for (int i = 0; i < STEPS; ++i) b[j * PARTS + q][i] = i * 64 < left ? load16(src + i * 64) : zero;
+            }
+          }
+          bp[j] += CHUNK;
+        }
     }
     if (!__all_sync(0xffffffffu, mbar_wait(&sm->ring_full[warp][tk.stage], tk.phase, p.timeout_ns, &sm->abort_flag,
                                            p.status)))
       return false;
-    const uint8_t* slot = sm->ring[warp][tk.stage];
-    const bool two = box + 1 < it.hi;  // the second box is there
+    const uint8_t* slot = ring + tk.stage * STAGE_BYTES;
     uint4 lo[STEPS], hi[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      const uint8_t* at = slot + (i >> 1) * BOX_BYTES + ((i & 1) ? at1 : at0);
-      lo[i] = i < 2 || two ? load16(at) : zero;
-      hi[i] = i < 2 || two ? load16(at + 8 * BOX) : zero;
+      const uint8_t* at = slot + ((i & 1) ? at1 : at0) + (i >> 1) * BOX_BYTES;
+      lo[i] = load16(at);
+      hi[i] = load16(at + 8 * BOX);
     }
     if (++tk.stage == NST) {
       tk.stage = 0;
@@ -371,9 +387,14 @@ __device__ __forceinline__ bool item_products(T (&acc)[NT][4], int k_bytes, cons
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-          mma_step(acc[j], lo[i], hi[i], EARLY ? b[j * PARTS + q][i] : token(j, q, i));
+        for (int i = 0; i < STEPS; ++i) {
+          if (EARLY)
+            mma_step(acc[j], lo[i], hi[i], b[j * PARTS + q][i]);
+          else
+            mma_step(acc[j], lo[i], hi[i], bp[j] && i * 64 < left ? load16(bp[j] + q * b_part + i * 64) : zero);
+        }
       }
+      if (!EARLY && bp[j]) bp[j] += CHUNK;
     }
   }
   return true;
@@ -381,17 +402,18 @@ __device__ __forceinline__ bool item_products(T (&acc)[NT][4], int k_bytes, cons
 
 // Take this warp's items of phase PH and leave their sums at dst[(slice * R + row) * ld + column], column b's 16 rows
 // (gated: gate rows at b * 8, up rows ph.up_row on).
-template <class T, int PH, int PARTS, class NextFn>
+template <class T, int PH, int PARTS, class NextFn, class PushedFn>
 __device__ __forceinline__ void run_items(const Params& p, const uint8_t* b_base, size_t b_part, T* dst, int ld, int R,
-                                          Taken& tk, Smem* sm, NextFn next) {
+                                          Taken& tk, Smem* sm, NextFn next, PushedFn pushed) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Phase& ph = sm->ph[PH];
   const int base = PH == 0 ? 0 : sm->ph[0].items;
   const int hi_col = ph.up_row != 0 ? ph.up_row : ROWS / 2;
   for (;;) {
-    __syncwarp();
+    if (pushed() == tk.head) return;  // the stream holds a ticket of the next phase
+    __syncwarp();                     // lane 0's entry is there for every lane
     const int ticket = sm->queue[warp][tk.head & (QUEUE - 1)];
-    if (ticket - base >= ph.items) return;  // the next phase's, or none
+    if (ticket == NO_ITEM) return;
     ++tk.head;
     const Item it = item_at(ph, ticket - base);
     const bool shared = it.j < p.n_shared;
@@ -878,12 +900,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   // the shared experts' weights need no routing: their items fill the ring behind the barrier
   Stream st;
   st.ticket = warp * (int)gridDim.x + (int)blockIdx.x;
-  st.next = NO_ITEM;
+  st.next = 0;
   st.stage = st.issued = st.pushed = 0;
+  const uint64_t pol = l2_policy_evict_first();
   int known = (p.n_shared * sm->ph[0].units) << p.s_log[0];
   if (lane == 0) {
     stream_begin(st, known, p, sm);
-    while (st.issued < NST && st.ready) stream_issue(st, &tm1, &tm2, known, p, sm);
+    while (st.issued < NST && st.ready) stream_issue(st, &tm1, &tm2, known, pol, p, sm);
   }
   Taken tk{0, 0u, 0};
   bool ok = grid_wait(&p.bar[0], p, sm);
@@ -894,17 +917,27 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int n_exp = p.n_shared + sm->n_touched;
     if (tid < 2) sm->ph[tid].items = (n_exp * sm->ph[tid].units) << p.s_log[tid];
     __syncthreads();
-    known = NO_ITEM;
+    // Phase 2's weights wait until the CTA has arrived at the end of phase 1: their loads would hold up the stores, the
+    // tickets and the barrier of a memory system that is busy with the last items of phase 1.
+    known = sm->ph[0].items;
     if (lane == 0) {
       if (!st.ready) stream_begin(st, known, p, sm);
-      while (st.issued < NST && st.ready) stream_issue(st, &tm1, &tm2, known, p, sm);
+      while (st.issued < NST && st.ready) stream_issue(st, &tm1, &tm2, known, pol, p, sm);
     }
-    auto next = [&]() { stream_issue(st, &tm1, &tm2, known, p, sm); };
+    auto pushed = [&]() { return __shfl_sync(0xffffffffu, st.pushed, 0); };
+    auto next = [&]() { stream_issue(st, &tm1, &tm2, known, pol, p, sm); };
     const int R = p.T * (p.k + p.n_shared);
 
     // phase 1
-    run_items<T, 0, 1>(p, I8 ? p.xq : p.x, 0, reinterpret_cast<T*>(p.u), f1, R, tk, sm, next);
-    ok = grid_barrier(&p.bar[1], p, sm);
+    run_items<T, 0, 1>(p, I8 ? p.xq : p.x, 0, reinterpret_cast<T*>(p.u), f1, R, tk, sm, next, pushed);
+    grid_arrive(&p.bar[1]);
+    known = NO_ITEM;
+    if (lane == 0) {
+      const int full = st.issued + NST;
+      stream_begin(st, known, p, sm);
+      while (st.issued < full && st.ready) stream_issue(st, &tm1, &tm2, known, pol, p, sm);
+    }
+    ok = grid_wait(&p.bar[1], p, sm);
     if (ok) {
       if (I8)
         code_hidden(p, sm, R);
@@ -914,7 +947,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // phase 2
     if (ok) {
-      run_items<T, 1, I8 ? 1 : 2>(p, p.h, (size_t)R * p.f * 2, reinterpret_cast<T*>(p.y), p.d, R, tk, sm, next);
+      run_items<T, 1, I8 ? 1 : 2>(p, p.h, (size_t)R * p.f * 2, reinterpret_cast<T*>(p.y), p.d, R, tk, sm, next, pushed);
       ok = grid_barrier(&p.bar[3], p, sm);
     }
     if (ok) finish_out<I8>(p, sm, R);
@@ -933,14 +966,14 @@ struct Layout {
   int s_log[2];
 };
 
-// log2 of the K slices of a matrix, for `units` blocks of 16 rows.  A phase ends when the last warp's last item does, so
+// log2 of the K slices of a matrix of nch chunks, for `units` blocks of 16 rows.  A phase ends when the last warp's last item does, so
 // an item should be short beside the phase: at least three items for each of 2368 warps, and as long as they are fewer
-// than sixteen each, at most 16 boxes of K (about 12 us).  Every item costs a ticket, its places and its partial sums,
-// so it keeps at least four boxes.  (32 tokens, SwiGLU, d 4096: items of 64 boxes left the first SM idle for 34 us.)
-inline int slices_log(double units, int nbox) {
+// than sixteen each, at most 8 chunks of K (about 12 us).  Every item costs a ticket, its places and its partial sums,
+// so it keeps at least two chunks.  (32 tokens, SwiGLU, d 4096: items of 32 chunks left the first SM idle for 34 us.)
+inline int slices_log(double units, int nch) {
   int s = 0;
-  while ((1 << (s + 1)) <= S_MAX && (nbox >> (s + 1)) >= 4 &&
-         (units * (1 << s) < 3.0 * 2368 || ((nbox >> s) > 16 && units * (1 << s) < 16.0 * 2368)))
+  while ((1 << (s + 1)) <= S_MAX && (nch >> (s + 1)) >= 2 &&
+         (units * (1 << s) < 3.0 * 2368 || ((nch >> s) > 8 && units * (1 << s) < 16.0 * 2368)))
     ++s;
   return s;
 }
@@ -957,8 +990,8 @@ inline Layout layout_of(int T, int d, int f, int n_routed, int n_shared, int k, 
   double miss = 1.0;
   for (int t = 0; t < T; ++t) miss *= 1.0 - (double)k / n_routed;
   const double experts = n_shared + n_routed * (1.0 - miss);
-  l.s_log[0] = slices_log(experts * (f / (swiglu ? ROWS / 2 : ROWS)), (d * elem + BOX - 1) / BOX);
-  l.s_log[1] = slices_log(experts * (d / ROWS), (f * elem + BOX - 1) / BOX);
+  l.s_log[0] = slices_log(experts * (f / (swiglu ? ROWS / 2 : ROWS)), (d * elem + CHUNK - 1) / CHUNK);
+  l.s_log[1] = slices_log(experts * (d / ROWS), (f * elem + CHUNK - 1) / CHUNK);
   const size_t R = (size_t)T * (k + n_shared);
   l.bar = take(8 * sizeof(unsigned int));
   l.logits = take((size_t)KS_MAX * T * E_LD * sizeof(float));
@@ -970,6 +1003,20 @@ inline Layout layout_of(int T, int d, int f, int n_routed, int n_shared, int k, 
   l.y = take((R * d * sizeof(float)) << l.s_log[1]);
   l.bytes = at;
   return l;
+}
+
+// Tensor map of expert matrices [E, rows, K], whose loads bring a chunk of 16 rows (gated: 8 gate rows and the 8 matching
+// up rows, `rows` being both halves) as STAGE_BYTES: boxes of 128 bytes side by side in K.
+inline int weight_map(CUtensorMap* map, const void* w, bool int8, int K, int rows, int E, bool gated, int* plain) {
+  const int elem = int8 ? 1 : 2, box = BOX / elem;
+  const uint64_t row = (uint64_t)K * elem;
+  *plain = row % BOX != 0;
+  if (*plain) return encode_tmap_u8(map, w, 3, K, rows, E, BOX, gated ? ROWS / 2 : ROWS);  // 8-bit rows alone
+  const uint64_t half = gated ? rows / 2 : rows;
+  const uint64_t dims[5] = {(uint64_t)box, half, gated ? 2ull : 1ull, row / BOX, (uint64_t)E};
+  const uint64_t strides[4] = {row, half * row, BOX, (uint64_t)rows * row};
+  const uint32_t boxes[5] = {(uint32_t)box, (uint32_t)(gated ? ROWS / 2 : ROWS), gated ? 2u : 1u, CHUNK / BOX, 1};
+  return encode_tmap_5d(map, w, elem, dims, strides, boxes);
 }
 
 template <bool I8>
@@ -1011,7 +1058,6 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
   p.w_r = reinterpret_cast<const uint8_t*>(w_router);
   p.bias = bias;
   p.offset = logit_offset;
-  p.elem = I8 ? 1 : 2;
   p.w1s = w1s;
   p.w2s = w2s;
   p.T = T;
@@ -1039,11 +1085,9 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
   p.s_log[0] = l.s_log[0];
   p.s_log[1] = l.s_log[1];
   CUtensorMap tm1, tm2;
-  constexpr auto encode = I8 ? encode_tmap_u8 : encode_tmap_bf16;
-  const uint32_t box = BOX / p.elem, E = n_routed + n_shared;
-  if ((rc = encode(&tm1, w1, 3, d, p.swiglu ? 2 * d_ff : d_ff, E, box, p.swiglu ? ROWS / 2 : ROWS)) != MOE_OK)
-    return rc;
-  if ((rc = encode(&tm2, w2, 3, d_ff, d, E, box, ROWS)) != MOE_OK) return rc;
+  const int f1 = p.swiglu ? 2 * d_ff : d_ff;
+  if ((rc = weight_map(&tm1, w1, I8, d, f1, n_routed + n_shared, p.swiglu != 0, &p.plain_map[0])) != MOE_OK) return rc;
+  if ((rc = weight_map(&tm2, w2, I8, d_ff, d, n_routed + n_shared, false, &p.plain_map[1])) != MOE_OK) return rc;
   const int rg_n = (n_routed + n_shared + ROWS - 1) / ROWS;
   const int nch_r = (d * 2 + BOX - 1) / BOX;
   // a chunk of K for every warp, in slices of as many CTAs as there are (every slice is read again by every

@@ -33,6 +33,10 @@ int encode_tmap_u8(CUtensorMap* map, const void* base, int rank, uint64_t dim0, 
 int encode_tmap_u8_plain(CUtensorMap* map, const void* base, uint64_t dim0, uint64_t dim1, uint32_t box0,
                          uint32_t box1);
 
+// A five-dimensional tensor of 2- or 1-byte elements with its own byte strides (dims[0] contiguous), 128-byte swizzle.
+int encode_tmap_5d(CUtensorMap* map, const void* base, int elem_bytes, const uint64_t dims[5],
+                   const uint64_t strides[4], const uint32_t box[5]);
+
 // Limit on device-side waits for kernels launched from now on.
 uint64_t wait_timeout_ns();
 
