@@ -379,9 +379,6 @@ __device__ __forceinline__ bool item_products(T (&acc)[NT][4], int k_bytes, cons
       tk.stage = 0;
       tk.phase ^= 1u;
     }
-    __syncwarp();  // every lane has its pieces: the stage may be filled again
-    if (lane == 0) next();
-    __syncwarp();
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -396,6 +393,11 @@ __device__ __forceinline__ bool item_products(T (&acc)[NT][4], int k_bytes, cons
       }
       if (!EARLY && bp[j]) bp[j] += CHUNK;
     }
+    // The stage may be filled again now, and not before: the products needed every lane's pieces in registers.  A warp
+    // barrier right behind the loads would order no more than their issue, and the copy writes by another path.
+    __syncwarp();
+    if (lane == 0) next();
+    __syncwarp();
   }
   return true;
 }

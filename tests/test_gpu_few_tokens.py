@@ -96,16 +96,23 @@ def test_matches_the_layer_in_64_bits(case, int8):
 
 
 @pytest.mark.parametrize("int8", [False, True], ids=["bf16", "int8"])
-def test_equal_inputs_give_equal_bits(int8):
-    p = make(13, 1024, 512, 48, 2, 6, "swiglu", seed=5)
+@pytest.mark.parametrize("case", [(13, 1024, 512, 48, 2, 6, "swiglu"), (2, 4096, 2048, 6, 1, 2, "swiglu"),
+                                  (1, 2048, 1024, 16, 2, 4, "gelu"), (40, 512, 256, 20, 2, 5, "gelu")],
+                         ids=lambda c: "T{}d{}f{}n{}s{}k{}{}".format(*c))
+def test_equal_inputs_give_equal_bits(case, int8):
+    """Hundreds of launches, each of whose items land on other warps: a race on a ring stage or a counter would show."""
+    p = make(*case, seed=5)
     p = to_int8(p) if int8 else p
     a, b = Call(p)(), Call(p)
     b.scratch.fill_(0x3c)
-    for _ in range(20):
+    different = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        b.out.fill_(float("nan"))
         b()
-    torch.cuda.synchronize()
-    for u, v in ((a.out, b.out), (a.gates, b.gates), (a.idx, b.idx), (a.counts, b.counts)):
-        assert torch.equal(u, v)
+        for u, v in ((a.out, b.out), (a.gates, b.gates), (a.idx, b.idx), (a.counts, b.counts)):
+            different += (u != v).sum()
+    a.check()
+    assert int(different) == 0
 
 
 def test_two_calls_at_once_on_two_streams():
