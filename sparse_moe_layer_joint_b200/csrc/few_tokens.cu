@@ -404,7 +404,7 @@ __device__ __forceinline__ bool item_products(T (&acc)[NT][4], int k_bytes, cons
 
 // Take this warp's items of phase PH and leave their sums at dst[(slice * R + row) * ld + column], column b's 16 rows
 // (gated: gate rows at b * 8, up rows ph.up_row on).
-template <class T, int PH, int PARTS, class NextFn, class PushedFn>
+template <class T, int PH, int PARTS, int NTM, class NextFn, class PushedFn>
 __device__ __forceinline__ void run_items(const Params& p, const uint8_t* b_base, size_t b_part, T* dst, int ld, int R,
                                           Taken& tk, Smem* sm, NextFn next, PushedFn pushed) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -440,15 +440,19 @@ __device__ __forceinline__ void run_items(const Params& p, const uint8_t* b_base
         }
       return true;
     };
-    bool ok;
-    if (n_e <= 8)
+    bool ok = false;
+    if (n_e <= 8) {
       ok = go(std::integral_constant<int, 1>{});
-    else if (n_e <= 16)
-      ok = go(std::integral_constant<int, 2>{});
-    else if (n_e <= 32)
-      ok = go(std::integral_constant<int, 4>{});
-    else
-      ok = go(std::integral_constant<int, NT_MAX>{});
+    } else if constexpr (NTM > 1) {
+      if (n_e <= 16) {
+        ok = go(std::integral_constant<int, 2>{});
+      } else if constexpr (NTM > 2) {
+        if (n_e <= 32)
+          ok = go(std::integral_constant<int, 4>{});
+        else
+          ok = go(std::integral_constant<int, NTM>{});
+      }
+    }
     if (!ok) return;
   }
 }
@@ -472,8 +476,10 @@ __device__ __forceinline__ void u_at(const Params& p, int R, int f1, int r, int 
   using T = typename AccT<I8>::type;
   const int S = 1 << p.s_log[0];
   const uint4* at = reinterpret_cast<const uint4*>(p.u + (size_t)r * f1 + c);
+  float4 w4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (I8) w4 = __ldg(reinterpret_cast<const float4*>(ws + c));  // from HBM: ahead of the sums, which are in L2
   T a[4] = {0, 0, 0, 0};
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < S; ++s) {
     const uint4 w = __ldcg(at + (size_t)s * R * f1 / 4);
     if constexpr (I8) {
@@ -488,8 +494,9 @@ __device__ __forceinline__ void u_at(const Params& p, int R, int f1, int r, int 
       a[3] += __uint_as_float(w.w);
     }
   }
+  const float m[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = I8 ? (float)a[i] * (xs * __ldg(ws + c + i)) : (float)a[i];
+  for (int i = 0; i < 4; ++i) v[i] = I8 ? (float)a[i] * (xs * m[i]) : (float)a[i];
 }
 
 template <bool I8>
@@ -638,6 +645,7 @@ __device__ __forceinline__ void finish_out(const Params& p, const Smem* sm, int 
 }
 
 // Phase 0: partial logits of 16 router rows over one slice of K, all tokens.
+template <int NTM>
 __device__ __forceinline__ void router_partial(const Params& p, Smem* sm) {
   const int E = p.n_routed + p.n_shared;
   const int rg_n = (E + ROWS - 1) / ROWS;
@@ -652,16 +660,16 @@ __device__ __forceinline__ void router_partial(const Params& p, Smem* sm) {
     const int r0 = min(rg * ROWS + (lane >> 2), E - 1), r1 = min(rg * ROWS + (lane >> 2) + 8, E - 1);
     const uint8_t* a0 = p.w_r + (size_t)r0 * k_bytes + (lane & 3) * 16;
     const uint8_t* a1 = p.w_r + (size_t)r1 * k_bytes + (lane & 3) * 16;
-    float acc[NT_MAX][4];
+    float acc[NTM][4];
 #pragma unroll
-    for (int j = 0; j < NT_MAX; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+    for (int j = 0; j < NTM; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
     for (int c = c_lo + warp; c < c_hi; c += WARPS) {
       const int off = c * BOX;
       const bool second = off + 64 < k_bytes;
       const uint4 lo0 = load16(a0 + off), hi0 = load16(a1 + off);
       const uint4 lo1 = second ? load16(a0 + off + 64) : zero, hi1 = second ? load16(a1 + off + 64) : zero;
 #pragma unroll
-      for (int j = 0; j < NT_MAX; ++j) {
+      for (int j = 0; j < NTM; ++j) {
         if (j < nt) {
           const int t = j * 8 + (lane >> 2);
           const uint8_t* b = p.x + (size_t)t * k_bytes + (lane & 3) * 16 + off;
@@ -675,8 +683,8 @@ __device__ __forceinline__ void router_partial(const Params& p, Smem* sm) {
     // the sum over the warps, through the ring's memory (the stream has not begun)
     float* red = reinterpret_cast<float*>(sm->ring);
 #pragma unroll
-    for (int j = 0; j < NT_MAX; ++j)
-      if (j < nt) red_store(red + (warp * NT_MAX + j) * RED_TILE, acc[j], lane);
+    for (int j = 0; j < NTM; ++j)
+      if (j < nt) red_store(red + (warp * NTM + j) * RED_TILE, acc[j], lane);
     __syncthreads();
     for (int i = tid; i < p.T * ROWS; i += THREADS) {
       const int col = i >> 4, r = i & 15;
@@ -684,7 +692,7 @@ __device__ __forceinline__ void router_partial(const Params& p, Smem* sm) {
       const float* at = red + (col >> 3) * RED_TILE + (col & 7) * RED_COL + r;
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) v += at[w * NT_MAX * RED_TILE];
+      for (int w = 0; w < WARPS; ++w) v += at[w * NTM * RED_TILE];
       if (e < E) p.logits[((size_t)ks * p.T + col) * E_LD + e] = v;
     }
     __syncthreads();
@@ -867,7 +875,9 @@ __device__ __forceinline__ bool route_all(const Params& p, Smem* sm) {
   return true;
 }
 
-template <bool I8>
+// NTM: tiles of 8 tokens an expert can have, 1, 2 or 8 by the call's T.  (The code for more than two needs more registers
+// than there are; with it one token at d 7168, d_ff 2048 took 94 us instead of 91.)
+template <bool I8, int NTM>
 __global__ void __launch_bounds__(THREADS, 1)
     few_tokens_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,
                       const Params p) {
@@ -896,7 +906,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   // phase 0
   if (I8) code_tokens(p, sm);
-  router_partial(p, sm);
+  router_partial<NTM>(p, sm);
   fence_proxy_async_smem();  // the ring's memory was the router's: TMA writes come after
   grid_arrive(&p.bar[0]);
   // the shared experts' weights need no routing: their items fill the ring behind the barrier
@@ -926,12 +936,22 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!st.ready) stream_begin(st, known, p, sm);
       while (st.issued < NST && st.ready) stream_issue(st, &tm1, &tm2, known, pol, p, sm);
     }
+    if (I8) {
+      // the channel scales of the experts in use, which a few CTAs need at once later, into L2 meanwhile
+      for (int j = (int)blockIdx.x; j < n_exp; j += (int)gridDim.x) {
+        const int e = expert_at(p, sm, j);
+        for (int i = tid; i < (f1 + p.d) / 32; i += THREADS) {
+          const float* a = i < f1 / 32 ? p.w1s + (size_t)e * f1 + i * 32 : p.w2s + (size_t)e * p.d + (i - f1 / 32) * 32;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(a));
+        }
+      }
+    }
     auto pushed = [&]() { return __shfl_sync(0xffffffffu, st.pushed, 0); };
     auto next = [&]() { stream_issue(st, &tm1, &tm2, known, pol, p, sm); };
     const int R = p.T * (p.k + p.n_shared);
 
     // phase 1
-    run_items<T, 0, 1>(p, I8 ? p.xq : p.x, 0, reinterpret_cast<T*>(p.u), f1, R, tk, sm, next, pushed);
+    run_items<T, 0, 1, NTM>(p, I8 ? p.xq : p.x, 0, reinterpret_cast<T*>(p.u), f1, R, tk, sm, next, pushed);
     grid_arrive(&p.bar[1]);
     known = NO_ITEM;
     if (lane == 0) {
@@ -949,7 +969,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     // phase 2
     if (ok) {
-      run_items<T, 1, I8 ? 1 : 2>(p, p.h, (size_t)R * p.f * 2, reinterpret_cast<T*>(p.y), p.d, R, tk, sm, next, pushed);
+      run_items<T, 1, I8 ? 1 : 2, NTM>(p, p.h, (size_t)R * p.f * 2, reinterpret_cast<T*>(p.y), p.d, R, tk, sm, next, pushed);
       ok = grid_barrier(&p.bar[3], p, sm);
     }
     if (ok) finish_out<I8>(p, sm, R);
@@ -1031,7 +1051,7 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
   if (I8 && (!w1s || !w2s)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(w1) || !aligned16(w2) || !aligned16(out) ||
       !aligned16(scratch) || !aligned4(bias) || !aligned4(logit_offset) || !aligned4(topk_idx) || !aligned4(gates) ||
-      !aligned4(counts) || !aligned4(w1s) || !aligned4(w2s))
+      !aligned4(counts) || !aligned16(w1s) || !aligned16(w2s))
     return MOE_ERR_INVALID_ARG;
   if (T < 0 || d <= 0 || d_ff <= 0 || n_routed < 1 || n_shared < 0 || top_k < 1) return MOE_ERR_INVALID_ARG;
   if (top_k > MOE_MAX_TOP_K || top_k > n_routed) return MOE_ERR_INVALID_ARG;
@@ -1050,7 +1070,7 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
   if (rc != MOE_OK) return rc;
   unsigned int* status = status_ptr();
   if (!status) return MOE_ERR_CUDA;
-  auto kfn = few_tokens_kernel<I8>;
+  auto kfn = T <= 8 ? few_tokens_kernel<I8, 1> : T <= 16 ? few_tokens_kernel<I8, 2> : few_tokens_kernel<I8, NT_MAX>;
   const size_t smem = sizeof(Smem) + 1024;
   if ((rc = ensure_smem_attr((const void*)kfn, smem)) != MOE_OK) return rc;
 
