@@ -110,6 +110,7 @@ struct GroupTables {
   int prefix[MOE_MAX_GROUPS + 1];  // prefix[g] = row tiles of groups < g
 };
 
+constexpr int I8_FEW_ROWS = 32;          // A rows of a small tile's loads in the 8-bit kernel
 constexpr int I8_COLS = BN / 2;          // accumulator columns an epilogue warp of the 8-bit kernel drains
 constexpr int I8_STAGE_BYTES = 32 * 64;  // and its staging of 32 rows by 32 bf16 columns
 
@@ -431,7 +432,11 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE, I8>::THREADS, 1)
     for (int tile = unit; active && tile < total_tiles && ok; tile += n_units) {
       const TileInfo ti = tile_info(tile, st->gt.prefix, G, p.n_tiles_n, p.n_major_rows);
       const Group gr = group_info(p, st->gt, ti.g);
-      const CUtensorMap* am = gr.a_map ? &tmA1 : &tmA0;
+      // 8-bit launches pass a second map of A with boxes of I8_FEW_ROWS rows, for tiles that have no more: the other
+      // rows of the stage keep what was there, and their sums are not stored
+      const bool few = I8 && gr.rows - ti.m * C::TILE_M <= I8_FEW_ROWS;
+      const CUtensorMap* am = gr.a_map || few ? &tmA1 : &tmA0;
+      const uint32_t tx_bytes = few ? C::TX_BYTES - C::A_BYTES + I8_FEW_ROWS * BK_I8 : C::TX_BYTES;
       const bool half = half_tile(p, gr, ti);
       // a half tile's CTA loads its usual 128-row box from its 64-row offset and uses the first 64 rows
       const int a_row = gr.a_base + ti.m * C::TILE_M + (int)rank * (half ? C::A_ROWS / 2 : C::A_ROWS);
@@ -460,7 +465,7 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE, I8>::THREADS, 1)
         if (lane == 0) ok = mbar_wait(&st->empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.status);
         if (gathering) ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
-        if (lane == 0 && leader) mbar_arrive_expect_tx(&st->full[stage], C::TX_BYTES);
+        if (lane == 0 && leader) mbar_arrive_expect_tx(&st->full[stage], tx_bytes);
         uint8_t* a_dst = smemA + stage * C::A_BYTES;
         if (gather) {
           __syncwarp();
@@ -929,7 +934,9 @@ int run_gemm(const GemmSpec& g, bool pair, int stages, int sms, long long tiles_
   constexpr auto encode = I8 ? encode_tmap_u8 : encode_tmap_bf16;
   constexpr uint32_t KE = I8 ? BK_I8 : BK;
   if ((rc = encode(&a0, g.a0, 2, K, g.a0_rows, 1, KE, g.a0_box_rows ? g.a0_box_rows : 128)) != MOE_OK) return rc;
-  if (g.a1) {
+  if (I8) {
+    if ((rc = encode(&a1, g.a0, 2, K, g.a0_rows, 1, KE, I8_FEW_ROWS)) != MOE_OK) return rc;
+  } else if (g.a1) {
     if ((rc = encode(&a1, g.a1, 2, K, g.a1_rows, 1, KE, 128)) != MOE_OK) return rc;
   } else {
     a1 = a0;

@@ -138,6 +138,7 @@ SIZES = [
     ([1100, 1500], 512, 640),
     ([700, 1, 900, 0, 512], 160, 7168),     # many stages
     ([256], 1056, 128),
+    ([32, 33, 31, 160, 161], 352, 400),     # around the 32 rows that a small tile's loads bring
 ]
 
 
@@ -187,17 +188,15 @@ def test_largest_sums_and_nan_scales():
     assert ((out - want).abs() <= tol)[keep].all()
 
 
-@pytest.mark.parametrize("env", [("MOE_GEMM_CTA", "1"), ("MOE_GEMM_CTA", "2"), ("MOE_GEMM_WIDE", "0"),
-                                 ("MOE_GEMM_HALF", "0"), ("MOE_GEMM_HALF", "1"), ("MOE_GEMM_STAGES", "3,3"),
-                                 ("MOE_GEMM_STAGES", "4,4")], ids=lambda e: f"{e[0]}={e[1]}")
+@pytest.mark.parametrize("rows", ["0", "1", "2", "64"])
 @pytest.mark.parametrize("epi", [0, 1, 2], ids=["none", "gelu", "swiglu"])
-def test_every_variant_gives_the_same_bits(monkeypatch, env, epi):
-    """The sums are exact, so tiles and stages cannot change a result."""
+def test_tile_order_does_not_change_the_bits(monkeypatch, rows, epi):
+    """The sums are exact, so the tiles' order cannot change a result."""
     counts, N, K = [300, 90, 0, 700], 320, 400
     aq, a_s, wq, w_s = operands(sum(counts), K, 4, 2 * N if epi == 2 else N, seed=8)
     off = np.concatenate([[0], np.cumsum(counts)]).tolist()
     a = gemm(aq, a_s, off, wq, w_s, N, epi)
-    monkeypatch.setenv(*env)
+    monkeypatch.setenv("MOE_GEMM_NMAJOR", rows)
     assert torch.equal(a, gemm(aq, a_s, off, wq, w_s, N, epi))
 
 
