@@ -197,7 +197,7 @@ __device__ __forceinline__ bool grid_wait(unsigned int* ctr, const Params& p, Sm
   if (threadIdx.x == 0) {
     const uint64_t t0 = globaltimer();
     for (uint32_t it = 1; ld_acquire(ctr) < gridDim.x; ++it) {
-      if ((it & 63u) == 0 && globaltimer() - t0 > p.timeout_ns) {
+      if ((it & 7u) == 0 && globaltimer() - t0 > p.timeout_ns) {
         set_status(p.status, MOE_STATUS_TIMEOUT);
         sm->abort_flag = 1;
         break;
@@ -974,11 +974,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (ok) finish_out<I8>(p, sm, R);
   }
-  // nothing may still be landing in shared memory (only a call that ran out of time can have chunks left)
+  // nothing may still be landing in shared memory (only a call that ran out of time can have chunks left; this wait
+  // is for copies that will land, however short the call's limit is)
   if (lane == 0) {
     int zero = 0;
+    const uint64_t limit = p.timeout_ns > 1000000000ull ? p.timeout_ns : 1000000000ull;
     for (int i = max(0, st.issued - NST); i < st.issued; ++i)
-      mbar_wait(&sm->ring_full[warp][i % NST], (i / NST) & 1, p.timeout_ns, &zero, p.status);
+      mbar_wait(&sm->ring_full[warp][i % NST], (i / NST) & 1, limit, &zero, p.status);
   }
 }
 

@@ -85,6 +85,9 @@ CASES = [
     (3, 2048, 768, 12, 2, 3, "gelu"),     # rows split over several warps
     (2, 4096, 2048, 6, 1, 2, "swiglu"),   # over all warps
     (1, 64, 4096, 4, 1, 4, "gelu"),       # wide hidden rows, narrow model
+    (1, 32768, 64, 3, 0, 2, "gelu"),      # the largest widths
+    (2, 64, 32768, 2, 1, 1, "swiglu"),
+    (16, 1408, 704, 30, 3, 5, "swiglu"),  # two full tiles, odd slices of K
 ]
 
 
@@ -225,6 +228,24 @@ def test_layer_few_tokens_against_its_many_token_form(precision, act):
     # h and y are each off by at most 2^-8 of their values (uniform: 2^-8 / sqrt 3 in the norm), out by 2^-8
     # on both sides; 8-bit codes of the rounded h differ where bf16 moved them over a step: at most 2^-8 again
     assert rel <= 2.0 ** -8 * np.sqrt(5), rel
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_whole():
+    """With a limit that few waits can keep (they look at the clock only now and then) a call ends in order: it is
+    whole or the status bit is set.  Nothing is left behind for the next call."""
+    c = Call(make(4, 1024, 512, 24, 1, 4, "gelu", seed=8))
+    moe.moe_set_wait_timeout_ns(1)
+    try:
+        for _ in range(3):
+            c()
+            torch.cuda.synchronize()
+            status = moe.moe_get_status()
+            assert status in (0, moe.MOE_STATUS_TIMEOUT)
+            if status == 0:
+                c.check()
+    finally:
+        moe.moe_set_wait_timeout_ns(2_000_000_000)
+    c().check()
 
 
 def test_layer_refuses_what_the_kernel_does_not_do():
