@@ -602,6 +602,16 @@ class MoELayer:
         moe_int8_quantize_rows(w1, E * f1, d, self.w1q, self.w1s, stream=stream)
         moe_int8_quantize_rows(w2, E * d, f, self.w2q, self.w2s, stream=stream)
 
+    def share_int8_weights(self, other: "MoELayer"):
+        """Use another layer's coded weights (a serving program's many-token and few-token layers keep one copy)."""
+        a, b = self.shape, other.shape
+        if not (self.int8 and other.int8) or other.w1q is None:
+            raise ValueError("both layers are precision=\"int8\", and the other has its weights")
+        if (a.d, a.d_ff, a.n_routed, a.n_shared, self.activation) != (b.d, b.d_ff, b.n_routed, b.n_shared,
+                                                                      other.activation):
+            raise ValueError("the layers' experts differ")
+        self.w1q, self.w1s, self.w2q, self.w2s = other.w1q, other.w1s, other.w2q, other.w2s
+
     def _forward_int8(self, x, main, ffn_events=None):
         s = self.shape
         T, d, f, k, R = s.T, s.d, s.d_ff, s.top_k, s.T * s.top_k

@@ -230,6 +230,38 @@ def test_layer_few_tokens_against_its_many_token_form(precision, act):
     assert rel <= 2.0 ** -8 * np.sqrt(5), rel
 
 
+def test_prefill_and_decode_layers_share_their_weights():
+    """The many-token layer of a prompt and the few-token layer of the next tokens, on one copy of 8-bit weights, with
+    the balancing bias running through both."""
+    T, d, f, n, ns, k = 200, 256, 128, 32, 2, 4
+    p = make(T, d, f, n, ns, k, "swiglu", seed=31)
+    t = {key: v.cuda() for key, v in p.items() if isinstance(v, torch.Tensor)}
+    prompt = moe.MoELayer(moe.LayerShape(T, d, f, n, ns, k), activation="swiglu", precision="int8")
+    step = moe.MoELayer(moe.LayerShape(5, d, f, n, ns, k), activation="swiglu", precision="int8", few_tokens=True)
+    with pytest.raises(ValueError):
+        step.share_int8_weights(prompt)  # it has none yet
+    prompt.set_int8_weights(t["w1"], t["w2"])
+    step.share_int8_weights(prompt)
+    assert step.w1q.data_ptr() == prompt.w1q.data_ptr()
+    bias = t["bias"].clone()
+    whole = prompt.forward(t["x"], t["w_r"], None, None, bias).float()
+    few = step.forward(t["x"][40:45].contiguous(), t["w_r"], None, None, bias).float()
+    assert torch.equal(step.topk_idx, prompt.topk_idx[40:45])
+    rel = ((few - whole[40:45]).norm() / few.norm()).item()
+    assert rel <= 2.0 ** -8 * 5 ** 0.5, rel  # h and y rounded to bf16 on the way of one of them, and both outputs
+    prompt.bias_update(bias, 1e-3)
+    b0 = bias.clone()
+    step.bias_update(bias, 1e-3)
+    torch.cuda.synchronize()
+    assert moe.moe_get_status() == 0
+    load = torch.bincount(step.topk_idx.flatten().long(), minlength=n)
+    want = b0 + torch.tensor(1e-3, device="cuda") * torch.sign((5 * k - n * load).float())
+    assert torch.equal(bias, want)
+    other = moe.MoELayer(moe.LayerShape(5, d, f, n, ns, k), precision="int8", few_tokens=True)
+    with pytest.raises(ValueError):
+        other.share_int8_weights(prompt)  # another activation
+
+
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_whole():
     """With a limit that few waits can keep (they look at the clock only now and then) a call ends in order: it is
     whole or the status bit is set.  Nothing is left behind for the next call."""
