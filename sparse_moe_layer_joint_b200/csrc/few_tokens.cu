@@ -974,13 +974,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (ok) finish_out<I8>(p, sm, R);
   }
-  // nothing may still be landing in shared memory (only a call that ran out of time can have chunks left; this wait
-  // is for copies that will land, however short the call's limit is)
+  // nothing may still be landing in shared memory (only a call that ran out of time can have chunks left)
   if (lane == 0) {
     int zero = 0;
-    const uint64_t limit = p.timeout_ns > 1000000000ull ? p.timeout_ns : 1000000000ull;
     for (int i = max(0, st.issued - NST); i < st.issued; ++i)
-      mbar_wait(&sm->ring_full[warp][i % NST], (i / NST) & 1, limit, &zero, p.status);
+      mbar_wait(&sm->ring_full[warp][i % NST], (i / NST) & 1, wind_down_ns(p.timeout_ns), &zero, p.status);
   }
 }
 

@@ -521,11 +521,11 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE, I8>::THREADS, 1)
         }
       }
     }
-    if (!ok && !PAIR && lane == 0) {
-      // wind down: let the copies already issued land before the CTA exits
+    if (!PAIR && lane == 0) {
+      // wind down: let the copies already issued land before the CTA exits (also when a later warp's wait ran out)
       int zero = 0;
       for (long i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
-        mbar_wait(&st->full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), p.timeout_ns, &zero, p.status);
+        mbar_wait(&st->full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), wind_down_ns(p.timeout_ns), &zero, p.status);
     }
   } else if (warp == 1) {
     // ================= MMA issuer (the pair's leader) =================
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE, I8>::THREADS, 1)
         mma_commit_pair(&st->drain, 0x1);
       else
         mma_commit(&st->drain);
-      mbar_wait(&st->drain, 0, p.timeout_ns, &zero, p.status);
+      mbar_wait(&st->drain, 0, wind_down_ns(p.timeout_ns), &zero, p.status);
     }
   } else if constexpr (I8) {
     epilogue_i8<EPI>(p, st, tmem_base, unit, n_units, total_tiles, G, warp, lane);

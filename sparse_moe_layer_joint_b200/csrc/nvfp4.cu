@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // wind down: let the copies already issued land before the CTA exits
         int zero = 0;
         for (long i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-          mbar_wait(&st->full[i % STAGES], (uint32_t)((i / STAGES) & 1), p.timeout_ns, &zero, p.status);
+          mbar_wait(&st->full[i % STAGES], (uint32_t)((i / STAGES) & 1), wind_down_ns(p.timeout_ns), &zero, p.status);
       }
     }
   } else if (warp == 1) {
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mma_commit_pair(&st->drain, 0x1);
       else
         mma_commit(&st->drain);
-      mbar_wait(&st->drain, 0, p.timeout_ns, &zero, p.status);
+      mbar_wait(&st->drain, 0, wind_down_ns(p.timeout_ns), &zero, p.status);
     }
   } else {
     // epilogue, EPI_WARPS warps: warp w reads TMEM lanes 32 * (w % 4) .. +31 (one tile row per thread)

@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!ok) {
         int zero = 0;
         for (long i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-          mbar_wait(&st->full[i % STAGES], (uint32_t)((i / STAGES) & 1), p.timeout_ns, &zero, p.status);
+          mbar_wait(&st->full[i % STAGES], (uint32_t)((i / STAGES) & 1), wind_down_ns(p.timeout_ns), &zero, p.status);
       }
     }
   } else if (warp == 1) {
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (ok) mma_commit(&st->tfull);
       int zero = 0;
       mma_commit(&st->drain);
-      mbar_wait(&st->drain, 0, p.timeout_ns, &zero, p.status);
+      mbar_wait(&st->drain, 0, wind_down_ns(p.timeout_ns), &zero, p.status);
     }
   } else {
     // ================= epilogue warps: park this CTA's logit tile in shared memory =================

@@ -85,6 +85,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   }
 }
 
+// Limit of the waits for a CTA's own copies and products in flight, which will finish, however short the call's limit
+// is: shared memory and TMEM must not be given back before.
+__device__ __forceinline__ uint64_t wind_down_ns(uint64_t timeout_ns) {
+  return timeout_ns > 1000000000ull ? timeout_ns : 1000000000ull;
+}
+
 // ----------------------------------------------------------------------------
 // TMA (tiled tensor copies global -> shared, completion on an mbarrier)
 // ----------------------------------------------------------------------------

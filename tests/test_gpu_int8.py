@@ -138,7 +138,8 @@ SIZES = [
     ([1100, 1500], 512, 640),
     ([700, 1, 900, 0, 512], 160, 7168),     # many stages
     ([256], 1056, 128),
-    ([32, 33, 31, 160, 161], 352, 400),     # around the 32 rows that a small tile's loads bring
+    ([32, 33, 31, 160, 161], 352, 400),     # around the 32 rows of a load of a group's last tile
+    ([64, 65, 96, 97, 224, 225], 288, 272),
 ]
 
 
