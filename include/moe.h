@@ -47,8 +47,7 @@
  *    (moe_router_topk still zeroes counts).
  *  - Host-only calls (no stream, nothing launched): moe_permute_scratch_bytes,
  *    moe_nvfp4_rows_capacity, moe_few_tokens_scratch_bytes, moe_capacity_for,
- *    moe_status_string,
- *    moe_set_wait_timeout_ns and the moe_ipc_* mappings.
+ *    moe_status_string, moe_set_wait_timeout_ns and the moe_ipc_* mappings.
  */
 #ifndef MOE_H
 #define MOE_H
@@ -397,7 +396,8 @@ int moe_int8_quantize_rows(const moe_bf16* x, long long rows, int K, int8_t* q, 
  * moe_int8_dispatch -- the 8-bit dispatch: each token's x row is coded once and
  * written to the rows of its routed experts.
  *   x          [T, d] bf16; token_row [T, top_k] from moe_permute (or
- *              moe_permute_capped: entries outside [0, n_rows), such as -1, are skipped)
+ *              moe_permute_capped: entries outside [0, n_rows), such as -1, are
+ *              skipped); no two tokens name the same row
  *   xq, xs     [n_rows, d] int8 and [n_rows] fp32 out: the routed experts' rows;
  *              rows no entry names are left as they were
  *   xq_tok, xs_tok  [T, d] int8 and [T] fp32 out: the same in token order, for the

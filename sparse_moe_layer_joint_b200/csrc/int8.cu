@@ -6,9 +6,9 @@
 // A row is held in registers between its maximum and its codes (VEC 16-byte
 // vectors a thread, TPR threads a row), so it is read once; rows of more than
 // 16384 values are read a second time, from L2.  A value costs one conversion, one
-// fma and three quarters of a byte permute (int8.cuh): 24570 rows of 2048 take 26.6
-// us (5.7 TB/s), the dispatch of 16384 tokens of 4096 to six experts 94 us (6.4
-// TB/s), one 2048 x 7168 matrix 12 us.
+// fma and three quarters of a byte permute (int8.cuh): 24570 rows of 2048 take 25.8
+// us (5.9 TB/s), the dispatch of 16384 tokens of 4096 to six experts 94 us (6.4
+// TB/s), one 2048 x 7168 matrix 7.9 us, the dispatch of 64 tokens of 7168 3.1 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
