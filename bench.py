@@ -697,16 +697,34 @@ def run_reference(args, w):
     }
 
 
+def _int8_rows(moe, rows, w1, w2, h):
+    """Codes and scales of the activation rows and the weights, and buffers for the hidden rows'."""
+    import torch
+
+    out = {}
+    for name, t in (("rows", rows), ("w1", w1), ("w2", w2), ("h", h)):
+        K = t.shape[-1]
+        q = torch.empty(t.shape, dtype=torch.int8, device=t.device)
+        scale = torch.empty(t.shape[:-1], dtype=torch.float32, device=t.device)
+        if name != "h":
+            moe.moe_int8_quantize_rows(t, t.numel() // K, K, q, scale)
+        out[name] = (q, scale)
+    return out
+
+
 def run_kernel_case(args):
     """The grouped expert GEMMs alone, on a prefill-shaped slice small enough to
     profile (32 experts x 1536 rows, d 7168, d_ff 2048: 3.5 GB on the device,
-    inputs larger than L2).  Prints one diagnostic JSON line (not a bench line)."""
+    inputs larger than L2), or the layer of one token (16 + 2 experts of that size).
+    Prints one diagnostic JSON line (not a bench line)."""
     import torch
 
     import sparse_moe_layer_joint_b200 as moe
 
     G, per, d, f = 32, 1536, 7168, 2048
-    if args.kernel_case == "nvfp4_decode":
+    if args.kernel_case.startswith("few_tokens"):
+        G, per = 18, 1  # 16 routed and 2 shared experts; the rows are the tokens
+    if args.kernel_case in ("nvfp4_decode", "int8_decode"):
         G, per = 64, 2  # decode-shaped: a couple of rows per expert, the weights streamed once
     n = G * per
     dev = torch.device("cuda", 0)
@@ -764,6 +782,26 @@ def run_kernel_case(args):
                                        hq, hsf, None, real, n if real is not None else 0)
             moe.moe_nvfp4_grouped_gemm(hq, hsf, offp, G, rows_cap, w2q, w2sf, g2, d, f, moe.MOE_NVFP4_EPI_BF16,
                                        None, None, y, offsets, n)
+    elif args.kernel_case.startswith("int8"):
+        q = _int8_rows(moe, rows, w1, w2, h)
+        s1, s2 = q["w1"], q["w2"]
+
+        def call():
+            moe.moe_int8_grouped_gemm(*q["rows"], offsets, G, n, 0, *s1, f, d, moe.MOE_INT8_EPI_GELU, h)
+            moe.moe_int8_quantize_rows(h, n, f, *q["h"])
+            moe.moe_int8_grouped_gemm(*q["h"], offsets, G, n, 0, *s2, d, f, moe.MOE_INT8_EPI_BF16, y)
+    elif args.kernel_case.startswith("few_tokens"):
+        int8 = args.kernel_case == "few_tokens_int8"
+        layer = moe.MoELayer(moe.LayerShape(1, d, f, G - 2, 2, 6), precision="int8" if int8 else "bf16",
+                             few_tokens=True)
+        if int8:
+            layer.set_int8_weights(w1, w2)
+        w_r = torch.empty((G, d), dtype=torch.bfloat16, device=dev)
+        mi.gpu_normal_bf16(w_r.data_ptr(), w_r.numel(), 0, mi.STREAM_WR, 0, d ** -0.5, s)
+        bias = torch.zeros(G - 2, device=dev)
+
+        def call():
+            layer.forward(rows[:1], w_r, w1, w2, bias)
     else:
         # comparison only (not the product path): the same two GEMMs per expert through cuBLAS
         xr, hr, yr = rows.view(G, per, d), h.view(G, per, f), y.view(G, per, d)
@@ -793,8 +831,11 @@ def run_kernel_case(args):
                           "host_us_per_call": round(host_us, 2),
                           "clocks": clk, "status": moe.moe_get_status()}), flush=True)
         return
+    if args.kernel_case.startswith("few_tokens"):
+        G, n, per = 8, 8, 1  # a token's experts
     flops = 2 * 2.0 * n * d * f
-    wbytes = G * 2 * d * f * (0.5 + 1 / 16 if args.kernel_case.startswith("nvfp4") else 2)
+    wbytes = G * 2 * d * f * (0.5 + 1 / 16 if args.kernel_case.startswith("nvfp4") else
+                              1 if args.kernel_case.startswith("int8") or args.kernel_case == "few_tokens_int8" else 2)
     print(json.dumps({"kernel_case": args.kernel_case, "experts": G, "rows_per_expert": per, "d": d, "d_ff": f,
                       "ms_per_call": round(ms, 4), "tflops": round(flops / (ms * 1e-3) / 1e12, 1),
                       "weight_gbs": round(wbytes / (ms * 1e-3) / 1e9, 1),
@@ -829,7 +870,7 @@ def main():
                     help="GEMM1 gathers the routed rows from x (TMA tile::gather4) instead of reading rows copied "
                          "by dispatch")
     ap.add_argument("--kernel-case", choices=["grouped_ffn", "grouped_ffn_cublas", "nvfp4_ffn", "nvfp4_decode",
-                                              "router"],
+                                              "int8_ffn", "int8_decode", "few_tokens", "few_tokens_int8", "router"],
                     default=None,
                     help="time one kernel alone on a small profiling case instead of the layer")
     args = ap.parse_args()
