@@ -30,8 +30,9 @@
 //                the CTAs (8-bit: the tokens' codes too); grid barrier, then every
 //                CTA selects for all T tokens itself (a warp a token; more than 8
 //                tokens are shared among the CTAs, with a barrier more)
-//             1  items of W1; grid barrier; the slices' sums, activation, and h in
-//                fp32 precision: as bf16 high and low parts (the product with both
+//             1  items of W1; grid barrier; the slices' sums (8-bit, few tokens: one
+//                sum that the slices were added to), activation, and h in fp32
+//                precision: as bf16 high and low parts (the product with both
 //                costs no extra weight traffic), or for 8-bit experts coded per row;
 //                grid barrier
 //             2  items of W2; grid barrier; out = the sum over the contributors'
@@ -48,7 +49,7 @@
 // stream at 6.1 to 7 TB/s; what remains beside them, 18 us at one token, is the
 // launch, the router and its barrier (9), the two barriers around the hidden rows
 // (8) and the last sums (5), less what the rings load meanwhile.  A layer of d 256
-// is those steps alone: 19 us.
+// is those steps alone: 18.6 us, where every CTA forms the few hidden rows itself.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -83,6 +84,10 @@ constexpr int MAX_CONTRIB = MOE_MAX_TOP_K + MOE_MAX_SHARED;
 constexpr int SELECT_ALL_T = 8;
 constexpr int QUEUE = 8;      // a warp's items between their first load and their products
 constexpr int NO_ITEM = 0x7fffffff;
+constexpr int ONE_SUM_T = 8;  // most tokens whose 8-bit experts' slices are added to one place (NTM 1)
+constexpr int OWN_SUMS = THREADS * 16;    // most sums of W1 x of which every CTA forms all hidden rows (bf16)
+constexpr int OWN_CODES = THREADS * 4;    // and most hidden values of which it codes all rows (8-bit)
+constexpr int OWN_ROWS = OWN_CODES / 64;
 
 struct Params {
   const uint8_t* x;    // [T, d] bf16
@@ -104,10 +109,10 @@ struct Params {
   float* logits;      // [KS][T][E_LD] partial logits
   uint8_t* xq;        // [T, d] token codes (int8)
   float* xs;          // [T]
-  float* u;           // [S1][R, f1] partial sums of W1 x (int32 for 8-bit experts)
+  float* u;           // [places][R, f1] sums of W1 x (int32 for 8-bit experts)
   uint8_t* h;         // bf16: [2][R, f] high and low parts; int8: [R, f] codes
   float* hs;          // [R] (int8)
-  float* y;           // [S2][R, d] partial sums of W2 h (int32 for 8-bit experts)
+  float* y;           // [places][R, d] sums of W2 h, right behind u
   int ks;             // K slices of the router phase
   int s_log[2];       // log2 of the K slices S1, S2
   uint64_t timeout_ns;
@@ -145,6 +150,8 @@ struct Smem {
   uint32_t key[SELECT_ALL_T * E_LD];
   int flag[WARPS];
   int abort_flag;
+  alignas(16) uint8_t own_h[OWN_SUMS * 4];  // the CTA's own hidden rows (bf16: high and low parts)
+  uint32_t own_max[OWN_ROWS];
 };
 static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory per CTA");
 static_assert(sizeof(float) * WARPS * NT_MAX * RED_TILE <= WARPS * NST * STAGE_BYTES, "the router's sums use the ring");
@@ -412,11 +419,30 @@ __device__ __forceinline__ bool item_products(T (&acc)[NT][4], int k_bytes, cons
   return true;
 }
 
-// Take this warp's items of phase PH and leave their sums at dst[(slice * R + row) * ld + column], column b's 16 rows
-// (gated: gate rows at b * 8, up rows ph.up_row on).
+// An item's sum goes to its slice's place, to be added up in order later.  8-bit experts, up to ONE_SUM_T tokens: int32
+// sums are exact in any order, so the slices are added to one place, zero at first, and the steps that wait for the sums
+// read one slice instead of four or eight (one token, SwiGLU, d 4096, d_ff 1024: 37.3 instead of 39.9 us; d 7168, d_ff
+// 2048: 54.8 instead of 55.5; with 13 tokens of d 2048, d_ff 768 the additions cost more than the reads, 83.6 instead of
+// 83.2).
+template <bool ONE_SUM, class T>
+__device__ __forceinline__ void leave(T* to, T v) {
+  if constexpr (ONE_SUM)
+    atomicAdd(to, v);
+  else
+    *to = v;
+}
+
+template <bool I8>
+__host__ __device__ __forceinline__ int places(int T, int s_log) {
+  return I8 && T <= ONE_SUM_T ? 1 : 1 << s_log;
+}
+
+// Take this warp's items of phase PH and leave their sums at dst[(slice * R + row) * ld + column] (ONE_SUM: dst[row * ld +
+// column]), column b's 16 rows (gated: gate rows at b * 8, up rows ph.up_row on).
 template <class T, int PH, int PARTS, int NTM, class NextFn, class PushedFn>
 __device__ __forceinline__ void run_items(const Params& p, const uint8_t* b_base, size_t b_part, T* dst, int ld, int R,
                                           Taken& tk, Smem* sm, NextFn next, PushedFn pushed) {
+  constexpr bool ONE_SUM = std::is_same<T, int>::value && NTM == 1;  // T <= ONE_SUM_T
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Phase& ph = sm->ph[PH];
   const int base = PH == 0 ? 0 : sm->ph[0].items;
@@ -433,7 +459,7 @@ __device__ __forceinline__ void run_items(const Params& p, const uint8_t* b_base
     const int n_e = shared ? p.T : sm->cnt[e];
     const int row0 = shared ? p.T * p.k + it.j * p.T : sm->pre[e];
     auto row = [&](int col) { return PH == 0 ? (shared ? col : (int)sm->row_tok[row0 + col]) : row0 + col; };
-    T* to = dst + ((size_t)it.s * R + row0) * ld + it.b * ph.row_mul + (lane >> 2);
+    T* to = dst + ((ONE_SUM ? 0 : (size_t)it.s * R) + row0) * ld + it.b * ph.row_mul + (lane >> 2);
     auto go = [&](auto n_tiles) {
       constexpr int NT = decltype(n_tiles)::value;
       T acc[NT][4];
@@ -444,8 +470,8 @@ __device__ __forceinline__ void run_items(const Params& p, const uint8_t* b_base
         for (int q = 0; q < 2; ++q) {
           const int col = j * 8 + 2 * (lane & 3) + q;
           if (col < n_e) {
-            to[(size_t)col * ld] = acc[j][q];
-            to[(size_t)col * ld + hi_col] = acc[j][q + 2];
+            leave<ONE_SUM>(to + (size_t)col * ld, acc[j][q]);
+            leave<ONE_SUM>(to + (size_t)col * ld + hi_col, acc[j][q + 2]);
           }
         }
       return true;
@@ -484,7 +510,7 @@ template <bool I8>
 __device__ __forceinline__ void u_at(const Params& p, int R, int f1, int r, int c, float xs, const float* ws,
                                      float (&v)[4]) {
   using T = typename AccT<I8>::type;
-  const int S = 1 << p.s_log[0];
+  const int S = places<I8>(p.T, p.s_log[0]);
   const uint4* at = reinterpret_cast<const uint4*>(p.u + (size_t)r * f1 + c);
   float4 w4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (I8) w4 = __ldg(reinterpret_cast<const float4*>(ws + c));  // from HBM: ahead of the sums, which are in L2
@@ -524,25 +550,41 @@ __device__ __forceinline__ void h_at(const Params& p, int R, int r, int c, float
   }
 }
 
-// h = act(W1 x) as bf16 high and low parts, four columns a thread over the whole grid.
+// h = act(W1 x) of four columns as bf16 high and low parts.
+__device__ __forceinline__ void hidden_parts(const Params& p, int R, int r, int c, uint2& hi, uint2& lo) {
+  float h[4];
+  h_at<false>(p, R, r, c, 0.0f, nullptr, h);
+  uint32_t a[2], b[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    a[q] = pack_bf16x2(h[2 * q], h[2 * q + 1]);
+    const float x = h[2 * q] - __uint_as_float(a[q] << 16), y = h[2 * q + 1] - __uint_as_float(a[q] & 0xffff0000u);
+    // an infinite or NaN high part has no low part
+    b[q] = pack_bf16x2(x - x == 0.0f ? x : 0.0f, y - y == 0.0f ? y : 0.0f);
+  }
+  hi = make_uint2(a[0], a[1]);
+  lo = make_uint2(b[0], b[1]);
+}
+
+// The hidden rows' parts, four columns a thread over the whole grid.
 __device__ __forceinline__ void finish_hidden(const Params& p, int R) {
   const int nv = p.f / 4;
   for (int i = (int)(threadIdx.x * gridDim.x + blockIdx.x); i < R * nv; i += THREADS * (int)gridDim.x) {
     const int r = i / nv, c = (i - r * nv) * 4;
-    float h[4];
-    h_at<false>(p, R, r, c, 0.0f, nullptr, h);
-    uint32_t hi[2], lo[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      hi[q] = pack_bf16x2(h[2 * q], h[2 * q + 1]);
-      float a = h[2 * q] - __uint_as_float(hi[q] << 16), b = h[2 * q + 1] - __uint_as_float(hi[q] & 0xffff0000u);
-      // an infinite or NaN high part has no low part
-      lo[q] = pack_bf16x2(a - a == 0.0f ? a : 0.0f, b - b == 0.0f ? b : 0.0f);
-    }
-    uint2* to = reinterpret_cast<uint2*>(p.h + ((size_t)r * p.f + c) * 2);
-    *to = make_uint2(hi[0], hi[1]);
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(to) + (size_t)R * p.f * 2) = make_uint2(lo[0], lo[1]);
+    uint2 hi, lo;
+    hidden_parts(p, R, r, c, hi, lo);
+    uint8_t* to = p.h + ((size_t)r * p.f + c) * 2;
+    *reinterpret_cast<uint2*>(to) = hi;
+    *reinterpret_cast<uint2*>(to + (size_t)R * p.f * 2) = lo;
   }
+}
+
+// The largest |v| as integers: NaN and infinity stay the largest.
+__device__ __forceinline__ uint32_t top_bits(const float (&v)[4]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  return m;
 }
 
 // 8-bit experts: a CTA a row, whose values stay in registers between their maximum and their codes (rows past
@@ -556,25 +598,18 @@ __device__ __forceinline__ void code_hidden(const Params& p, Smem* sm, int R) {
     row_owner(p, sm, r, e, t);
     const float xs = __ldcg(p.xs + t);
     const float* ws = p.w1s + (size_t)e * f1;
-    // |v| as integers: NaN and infinity stay the largest
-    auto top = [](const float (&v)[4]) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-      return m;
-    };
     uint32_t m = 0;
     float keep[HV][4];
 #pragma unroll
     for (int i = 0; i < HV; ++i)
       if (tid + i * THREADS < nv) {
         h_at<true>(p, R, r, (tid + i * THREADS) * 4, xs, ws, keep[i]);
-        m = max(m, top(keep[i]));
+        m = max(m, top_bits(keep[i]));
       }
     for (int c = tid + HV * THREADS; c < nv; c += THREADS) {
       float v[4];
       h_at<true>(p, R, r, c * 4, xs, ws, v);
-      m = max(m, top(v));
+      m = max(m, top_bits(v));
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) sm->flag[warp] = (int)m;
@@ -596,12 +631,56 @@ __device__ __forceinline__ void code_hidden(const Params& p, Smem* sm, int R) {
   }
 }
 
+// Few hidden values: every CTA forms all of them for itself, in its shared memory, and no barrier follows (2 tokens, d
+// 256, d_ff 128: 18.6 instead of 20.2 us in bf16, 18.7 instead of 19.8 in 8 bits).  More values a thread lose: with 32
+// for 8-bit experts one token at d 7168, d_ff 2048 took 63 us instead of 55, all SMs reading the same lines at once.
+template <bool I8>
+__device__ __forceinline__ bool own_rows(const Params& p, int R) {
+  if (I8) return (long long)R * p.f <= OWN_CODES;
+  return ((long long)R * (p.swiglu ? 2 * p.f : p.f) << p.s_log[0]) <= OWN_SUMS;
+}
+
+template <bool I8>
+__device__ __forceinline__ void own_hidden(const Params& p, Smem* sm, int R) {
+  const int nv = p.f / 4, tid = threadIdx.x;
+  if constexpr (I8) {  // four values a thread; f is a multiple of 64, so 16 neighbouring threads share a row
+    const int r = tid / nv, c = tid - r * nv;
+    float h[4];
+    if (r < R) {
+      int e, t;
+      row_owner(p, sm, r, e, t);
+      const int f1 = p.swiglu ? 2 * p.f : p.f;
+      h_at<true>(p, R, r, c * 4, __ldcg(p.xs + t), p.w1s + (size_t)e * f1, h);
+      uint32_t m = top_bits(h);
+      const uint32_t group = 0xffffu << (tid & 16);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(group, m, o));
+      if ((tid & 15) == 0) atomicMax(&sm->own_max[r], m);
+    }
+    __syncthreads();
+    if (r < R) {
+      const q8::RowScale rs = q8::row_scale(__uint_as_float(sm->own_max[r]));
+      reinterpret_cast<uint32_t*>(sm->own_h)[tid] = q8::code4_f32(h, rs);
+      if (blockIdx.x == 0 && c == 0) p.hs[r] = rs.scale;  // every CTA's last sums read it, a barrier later
+    }
+  } else {
+    for (int i = tid; i < R * nv; i += THREADS) {
+      const int r = i / nv, c = (i - r * nv) * 4;
+      uint2 hi, lo;
+      hidden_parts(p, R, r, c, hi, lo);
+      reinterpret_cast<uint2*>(sm->own_h)[i] = hi;
+      reinterpret_cast<uint2*>(sm->own_h)[R * nv + i] = lo;
+    }
+  }
+  __syncthreads();
+}
+
 // out[t, col] = sum over the contributors of gate * (sum of the slices).  A thread takes one contributor's four
 // neighbouring columns, GL threads (a power of two) one token's contributors, added up in a fixed tree.  (Short code: it
 // runs once, and instructions that are fetched for one use cost more than the loads they issue.)
 template <bool I8>
 __device__ __forceinline__ void finish_out(const Params& p, const Smem* sm, int R) {
-  const int G = p.k + p.n_shared, S = 1 << p.s_log[1];
+  const int G = p.k + p.n_shared, S = places<I8>(p.T, p.s_log[1]);
   const int gl = G > 8 ? 4 : G > 4 ? 3 : G > 2 ? 2 : G > 1 ? 1 : 0;  // log2 GL
   const int nv = p.d / 4, total = (p.T * nv) << gl;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -899,6 +978,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int f1 = p.swiglu ? 2 * p.f : p.f;
 
   if (tid < MOE_MAX_ROUTED) sm->mask[tid] = 0;
+  if (tid < OWN_ROWS) sm->own_max[tid] = 0;
   if (tid < WARPS) {
     for (int i = 0; i < NST; ++i) mbar_init(&sm->ring_full[tid][i], 1);
     fence_barrier_init();
@@ -915,6 +995,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 
   // phase 0
+  if (I8 && NTM == 1) {
+    // the sums of both phases begin at zero (they lie next to each other)
+    uint4* at = reinterpret_cast<uint4*>(p.u);
+    const int n = p.T * (p.k + p.n_shared) * ((f1 + p.d) / 4);
+    for (int i = (int)blockIdx.x * THREADS + tid; i < n; i += (int)gridDim.x * THREADS) at[i] = make_uint4(0, 0, 0, 0);
+  }
   if (I8) code_tokens(p, sm);
   router_partial<NTM>(p, sm);
   fence_proxy_async_smem();  // the ring's memory was the router's: TMA writes come after
@@ -970,16 +1056,22 @@ __global__ void __launch_bounds__(THREADS, 1)
       while (st.issued < full && st.ready) stream_issue(st, &tm1, &tm2, known, pol, p, sm);
     }
     ok = grid_wait(&p.bar[1], p, sm);
+    const bool own = NTM == 1 && own_rows<I8>(p, R);  // (more tokens have more rows; 64: the choice alone cost 3%)
     if (ok) {
-      if (I8)
-        code_hidden(p, sm, R);
-      else
-        finish_hidden(p, R);
-      ok = grid_barrier(&p.bar[2], p, sm);
+      if (own) {
+        own_hidden<I8>(p, sm, R);
+      } else {
+        if (I8)
+          code_hidden(p, sm, R);
+        else
+          finish_hidden(p, R);
+        ok = grid_barrier(&p.bar[2], p, sm);
+      }
     }
     // phase 2
     if (ok) {
-      run_items<T, 1, I8 ? 1 : 2, NTM>(p, p.h, (size_t)R * p.f * 2, reinterpret_cast<T*>(p.y), p.d, R, tk, sm, next, pushed);
+      run_items<T, 1, I8 ? 1 : 2, NTM>(p, own ? sm->own_h : p.h, (size_t)R * p.f * 2, reinterpret_cast<T*>(p.y), p.d, R,
+                                       tk, sm, next, pushed);
       ok = grid_barrier(&p.bar[3], p, sm);
     }
     if (ok) finish_out<I8>(p, sm, R);
@@ -998,9 +1090,9 @@ struct Layout {
   int s_log[2];
 };
 
-// log2 of the K slices of a matrix of nch chunks, for `units` blocks of 16 rows.  A phase ends when the last warp's last item does, so
-// an item should be short beside the phase: at least one and a half items for each of 2368 warps, and as long as they are fewer
-// than sixteen each, at most 8 chunks of K (about 12 us).  Every item costs a ticket, its places and its partial sums,
+// log2 of the K slices of a matrix of nch chunks, for `units` blocks of 16 rows.  A phase ends when the last warp's last
+// item does, so an item should be short beside the phase: at least one and a half items for each of 2368 warps, and as
+// long as they are fewer than sixteen each, at most 8 chunks of K (about 12 us).  Every item costs a ticket, its places and its partial sums,
 // so it keeps at least two chunks.  (32 tokens, SwiGLU, d 4096: items of 32 chunks left the first SM idle for 34 us.)
 inline int slices_log(double units, int nch) {
   int s = 0;
@@ -1029,10 +1121,11 @@ inline Layout layout_of(int T, int d, int f, int n_routed, int n_shared, int k, 
   l.logits = take((size_t)KS_MAX * T * E_LD * sizeof(float));
   l.xq = take((size_t)T * d);
   l.xs = take((size_t)T * sizeof(float));
-  l.u = take((R * (swiglu ? 2 * f : f) * sizeof(float)) << l.s_log[0]);
+  auto n_places = [&](int s_log) { return (size_t)(elem == 1 ? places<true>(T, s_log) : places<false>(T, s_log)); };
+  l.u = take(R * (swiglu ? 2 * f : f) * sizeof(float) * n_places(l.s_log[0]));
+  l.y = take(R * d * sizeof(float) * n_places(l.s_log[1]));
   l.h = take(R * f * sizeof(float));
   l.hs = take(R * sizeof(float));
-  l.y = take((R * d * sizeof(float)) << l.s_log[1]);
   l.bytes = at;
   return l;
 }
@@ -1080,7 +1173,9 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
   if (rc != MOE_OK) return rc;
   unsigned int* status = status_ptr();
   if (!status) return MOE_ERR_CUDA;
-  auto kfn = T <= 8 ? few_tokens_kernel<I8, 1> : T <= 16 ? few_tokens_kernel<I8, 2> : few_tokens_kernel<I8, NT_MAX>;
+  auto kfn = T <= ONE_SUM_T ? few_tokens_kernel<I8, 1>
+             : T <= 16      ? few_tokens_kernel<I8, 2>
+                            : few_tokens_kernel<I8, NT_MAX>;
   const size_t smem = sizeof(Smem) + 1024;
   if ((rc = ensure_smem_attr((const void*)kfn, smem)) != MOE_OK) return rc;
 

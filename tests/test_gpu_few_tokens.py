@@ -88,6 +88,10 @@ CASES = [
     (1, 32768, 64, 3, 0, 2, "gelu"),      # the largest widths
     (2, 64, 32768, 2, 1, 1, "swiglu"),
     (16, 1408, 704, 30, 3, 5, "swiglu"),  # two full tiles, odd slices of K
+    (1, 64, 1024, 4, 1, 1, "gelu"),       # around the hidden values that every CTA forms for itself
+    (1, 64, 1088, 4, 1, 1, "swiglu"),
+    (8, 128, 64, 9, 2, 2, "swiglu"),
+    (4, 1024, 128, 24, 0, 4, "gelu"),
 ]
 
 
