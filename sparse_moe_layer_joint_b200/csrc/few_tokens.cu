@@ -57,6 +57,7 @@
 
 #include <type_traits>
 
+#include "few_stream.h"
 #include "int8.cuh"
 #include "moe.h"
 #include "moe_internal.h"
@@ -67,7 +68,6 @@ namespace few {
 
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
-constexpr int NST = 2;        // ring stages (chunks) per warp
 constexpr int BOX = 128;      // bytes of K of one row a TMA box holds (one swizzle atom)
 constexpr int CHUNK = 256;    // and a chunk: two boxes side by side
 constexpr int STEPS = CHUNK / 64;  // 64-byte steps of K (two MMA instructions each)
@@ -82,8 +82,6 @@ constexpr int RED_COL = 20;   // floats per token column of a warp's logits tile
 constexpr int RED_TILE = 8 * RED_COL;
 constexpr int MAX_CONTRIB = MOE_MAX_TOP_K + MOE_MAX_SHARED;
 constexpr int SELECT_ALL_T = 8;
-constexpr int QUEUE = 8;      // a warp's items between their first load and their products
-constexpr int NO_ITEM = 0x7fffffff;
 constexpr int ONE_SUM_T = 8;  // most tokens whose 8-bit experts' slices are added to one place (NTM 1)
 constexpr int OWN_SUMS = THREADS * 16;    // most sums of W1 x of which every CTA forms all hidden rows (bf16)
 constexpr int OWN_CODES = THREADS * 4;    // and most hidden values of which it codes all rows (8-bit)
@@ -117,18 +115,6 @@ struct Params {
   int s_log[2];       // log2 of the K slices S1, S2
   uint64_t timeout_ns;
   unsigned int* status;
-};
-
-// One of the two phases: its matrices' items.  Item t (of the phase) is slice t % S of block b of the j-th
-// expert, t / S = j * units + b.
-struct Phase {
-  int k_bytes;  // bytes of a row
-  int nch;      // chunks of a row
-  int units;    // blocks of 16 rows per expert
-  int s_log;
-  int row_mul;  // first row of block b: b * row_mul
-  int up_row;   // gated: rows from a gate row to its up row, else 0
-  int items;    // of all its experts
 };
 
 struct Smem {
@@ -244,93 +230,51 @@ __device__ __forceinline__ Phase make_phase(int rows, int K, int elem, bool gate
   return ph;
 }
 
-// An item: slice s (chunks lo .. hi - 1) of block b of the j-th expert.
-struct Item {
-  int j, b, s, lo, hi;
-};
-
-__device__ __forceinline__ Item item_at(const Phase& ph, int t) {
-  Item it;
-  it.s = t & ((1 << ph.s_log) - 1);
-  const int u = t >> ph.s_log;
-  it.j = u / ph.units;
-  it.b = u - it.j * ph.units;
-  it.lo = (ph.nch * it.s) >> ph.s_log;
-  it.hi = (ph.nch * (it.s + 1)) >> ph.s_log;
-  return it;
-}
-
 __device__ __forceinline__ int expert_at(const Params& p, const Smem* sm, int j) {
   return j < p.n_shared ? p.n_routed + j : sm->list[j - p.n_shared];
 }
 
-// The warp's weight stream, kept by its lane 0: item by item, a chunk at a time.
-struct Stream {
-  int ticket;        // the item being loaded (or held)
-  unsigned int next; // the draw for the item after it, as the counter returned it: nothing may use it before it is needed
-  int phase;
-  int ch, hi;        // next chunk of the item, its end
-  int row, e;        // the item's first row, and expert
-  int stage, issued, pushed;
-  bool ready;        // the item's place is known
-};
+// What the stream (few_stream.h) reaches: the call's tickets, the warp's ring and queue, the matrices.
+struct StreamEnv {
+  const CUtensorMap* tm1;
+  const CUtensorMap* tm2;
+  uint64_t pol;
+  const Params& p;
+  Smem* sm;
 
-// Begin the stream's ticket: phase 1's items come first, then phase 2's.  Before the routing only the first
-// `known` items can be placed; the stream then stops with its ticket in hand.
-__device__ __forceinline__ void stream_begin(Stream& s, int known, const Params& p, Smem* sm) {
-  s.ready = false;
-  if (s.ticket >= known) return;
-  const int warp = threadIdx.x >> 5;
-  s.phase = s.ticket < sm->ph[0].items ? 0 : 1;
-  const Phase& ph = sm->ph[s.phase];
-  const int t = s.ticket - (s.phase ? sm->ph[0].items : 0);
-  const bool any = t < ph.items;
-  sm->queue[warp][s.pushed++ & (QUEUE - 1)] = any ? s.ticket : NO_ITEM;
-  if (!any) return;
-  const Item it = item_at(ph, t);
-  s.ch = it.lo;
-  s.hi = it.hi;
-  s.row = it.b * ph.row_mul;
-  s.e = expert_at(p, sm, it.j);
-  s.ready = true;
-  s.next = atomicAdd(p.bar + 4, 1u);
-}
+  __device__ __forceinline__ const Phase& phase(int i) const { return sm->ph[i]; }
+  __device__ __forceinline__ void queue(int at, int item) { sm->queue[threadIdx.x >> 5][at] = item; }
+  __device__ __forceinline__ int expert(int j) const { return expert_at(p, sm, j); }
+  __device__ __forceinline__ unsigned int draw() { return atomicAdd(p.bar + 4, 1u); }
+  // (a ring wait's flag is seen by every lane 0: a block barrier lies between the items and the next fill)
+  __device__ __forceinline__ bool ran_out() const { return sm->abort_flag != 0; }
+  __device__ __forceinline__ unsigned int warps() const { return gridDim.x * WARPS; }
 
-// Load the next chunk into the next stage, which the warp has read.  The matrices' maps have K as blocks of 128 bytes
-// next to each other in a dimension of their own, and the gate and up rows likewise, so that one load brings the whole
-// chunk; rows that are not whole blocks (8-bit, K an odd multiple of 64) take a plain map and a load a box.
-__device__ __forceinline__ void stream_issue(Stream& s, const CUtensorMap* tm1, const CUtensorMap* tm2, int known,
-                                             uint64_t pol, const Params& p, Smem* sm) {
-  if (!s.ready) return;
-  const CUtensorMap* map = s.phase == 0 ? tm1 : tm2;
-  const int warp = threadIdx.x >> 5;
-  uint8_t* dst = sm->ring[warp][s.stage];
-  uint64_t* bar = &sm->ring_full[warp][s.stage];
-  mbar_arrive_expect_tx(bar, STAGE_BYTES);  // what lies past the row's end arrives as zeros
-  if (!p.plain_map[s.phase]) {
-    tma_load_5d_hint(dst, map, bar, 0, s.row, 0, s.ch * (CHUNK / BOX), s.e, pol);
-  } else {
-    const int up_row = sm->ph[s.phase].up_row;
-    for (int h = 0; h < CHUNK / BOX; ++h) {
-      const int x = s.ch * CHUNK + h * BOX;
-      tma_load_3d_hint(dst + h * BOX_BYTES, map, bar, x, s.row, s.e, pol);
-      if (up_row != 0) tma_load_3d_hint(dst + h * BOX_BYTES + BOX_BYTES / 2, map, bar, x, s.row + up_row, s.e, pol);
+  // The matrices' maps have K as blocks of 128 bytes next to each other in a dimension of their own, and the gate and up
+  // rows likewise, so that one load brings the whole chunk; rows that are not whole blocks (8-bit, K an odd multiple of
+  // 64) take a plain map and a load a box.
+  __device__ __forceinline__ void load(const Stream& s) {
+    const CUtensorMap* map = s.phase == 0 ? tm1 : tm2;
+    const int warp = threadIdx.x >> 5;
+    uint8_t* dst = sm->ring[warp][s.stage];
+    uint64_t* bar = &sm->ring_full[warp][s.stage];
+    mbar_arrive_expect_tx(bar, STAGE_BYTES);  // what lies past the row's end arrives as zeros
+    if (!p.plain_map[s.phase]) {
+      tma_load_5d_hint(dst, map, bar, 0, s.row, 0, s.ch * (CHUNK / BOX), s.e, pol);
+    } else {
+      const int up_row = sm->ph[s.phase].up_row;
+      for (int h = 0; h < CHUNK / BOX; ++h) {
+        const int x = s.ch * CHUNK + h * BOX;
+        tma_load_3d_hint(dst + h * BOX_BYTES, map, bar, x, s.row, s.e, pol);
+        if (up_row != 0) tma_load_3d_hint(dst + h * BOX_BYTES + BOX_BYTES / 2, map, bar, x, s.row + up_row, s.e, pol);
+      }
     }
   }
-  ++s.issued;
-  s.stage = s.stage + 1 == NST ? 0 : s.stage + 1;
-  if (++s.ch >= s.hi) {
-    s.ticket = (int)(s.next + gridDim.x * WARPS);  // every warp's first item is its own number
-    stream_begin(s, known, p, sm);
-  }
-}
 
-// The consuming side, the same in every lane: the next chunk's stage and its phase bit, the next item's place in
-// the queue.
-struct Taken {
-  int stage;
-  uint32_t phase;
-  int head;
+  __device__ __forceinline__ void wait(int stage, uint32_t parity) {
+    int no_abort = 0;
+    mbar_wait(&sm->ring_full[threadIdx.x >> 5][stage], parity, wind_down_ns(p.timeout_ns), &no_abort, p.status);
+  }
 };
 
 // An item's products: its chunks of 16 weight rows against the expert's n_e token rows, NT tiles of 8.
@@ -392,10 +336,7 @@ __device__ __forceinline__ bool item_products(T (&acc)[NT][4], int k_bytes, cons
       lo[i] = load16(at);
       hi[i] = load16(at + 8 * BOX);
     }
-    if (++tk.stage == NST) {
-      tk.stage = 0;
-      tk.phase ^= 1u;
-    }
+    take(tk);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -1010,12 +951,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   st.ticket = warp * (int)gridDim.x + (int)blockIdx.x;
   st.next = 0;
   st.stage = st.issued = st.pushed = 0;
+  st.ready = false;
   const uint64_t pol = l2_policy_evict_first();
+  auto env = [&]() { return StreamEnv{&tm1, &tm2, pol, p, sm}; };  // (kept as one object it cost registers)
   int known = (p.n_shared * sm->ph[0].units) << p.s_log[0];
-  if (lane == 0) {
-    stream_begin(st, known, p, sm);
-    while (st.issued < NST && st.ready) stream_issue(st, &tm1, &tm2, known, pol, p, sm);
-  }
+  if (lane == 0) stream_start(st, known, env());
   Taken tk{0, 0u, 0};
   bool ok = grid_wait(&p.bar[0], p, sm);
   if (ok) {
@@ -1028,10 +968,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Phase 2's weights wait until the CTA has arrived at the end of phase 1: their loads would hold up the stores, the
     // tickets and the barrier of a memory system that is busy with the last items of phase 1.
     known = sm->ph[0].items;
-    if (lane == 0) {
-      if (!st.ready) stream_begin(st, known, p, sm);
-      while (st.issued < NST && st.ready) stream_issue(st, &tm1, &tm2, known, pol, p, sm);
-    }
+    if (lane == 0) stream_start(st, known, env());
     if (I8) {
       // the channel scales of the experts in use, which a few CTAs need at once later, into L2 meanwhile
       for (int j = (int)blockIdx.x; j < n_exp; j += (int)gridDim.x) {
@@ -1043,18 +980,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     auto pushed = [&]() { return __shfl_sync(0xffffffffu, st.pushed, 0); };
-    auto next = [&]() { stream_issue(st, &tm1, &tm2, known, pol, p, sm); };
+    auto next = [&]() { stream_issue(st, known, env()); };
     const int R = p.T * (p.k + p.n_shared);
 
     // phase 1
     run_items<T, 0, 1, NTM>(p, I8 ? p.xq : p.x, 0, reinterpret_cast<T*>(p.u), f1, R, tk, sm, next, pushed);
     grid_arrive(&p.bar[1]);
     known = NO_ITEM;
-    if (lane == 0) {
-      const int full = st.issued + NST;
-      stream_begin(st, known, p, sm);
-      while (st.issued < full && st.ready) stream_issue(st, &tm1, &tm2, known, pol, p, sm);
-    }
+    if (lane == 0) stream_next_phase(st, known, env());
     ok = grid_wait(&p.bar[1], p, sm);
     const bool own = NTM == 1 && own_rows<I8>(p, R);  // (more tokens have more rows; 64: the choice alone cost 3%)
     if (ok) {
@@ -1077,11 +1010,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (ok) finish_out<I8>(p, sm, R);
   }
   // nothing may still be landing in shared memory (only a call that ran out of time can have chunks left)
-  if (lane == 0) {
-    int zero = 0;
-    for (int i = max(0, st.issued - NST); i < st.issued; ++i)
-      mbar_wait(&sm->ring_full[warp][i % NST], (i / NST) & 1, wind_down_ns(p.timeout_ns), &zero, p.status);
-  }
+  if (lane == 0) stream_drain(st, env());
 }
 
 // Scratch layout: byte offsets of each part.
