@@ -200,7 +200,8 @@ __device__ __forceinline__ bool grid_wait(unsigned int* ctr, const Params& p, Sm
   if (threadIdx.x == 0) {
     const uint64_t t0 = globaltimer();
     for (uint32_t it = 1; ld_acquire(ctr) < gridDim.x; ++it) {
-      if ((it & 7u) == 0 && globaltimer() - t0 > p.timeout_ns) {
+      // (the clock: after the first poll, so that the shortest limit is noticed, then every eighth)
+      if ((it & 7u) == 1 && globaltimer() - t0 > p.timeout_ns) {
         set_status(p.status, MOE_STATUS_TIMEOUT);
         sm->abort_flag = 1;
         break;
