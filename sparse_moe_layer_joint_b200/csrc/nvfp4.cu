@@ -555,8 +555,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       }
-      if (!ok && !PAIR) {
-        // wind down: let the copies already issued land before the CTA exits
+      if (!PAIR) {
+        // wind down: let the copies already issued land before the CTA exits (also when a later warp's wait ran out)
         int zero = 0;
         for (long i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
           mbar_wait(&st->full[i % STAGES], (uint32_t)((i / STAGES) & 1), wind_down_ns(p.timeout_ns), &zero, p.status);

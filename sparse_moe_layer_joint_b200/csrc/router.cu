@@ -392,12 +392,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       long issued = 0;
-      bool ok = true;
       for (int kb = kb0; kb < kb0 + kb_per; ++kb) {
-        if (!mbar_wait(&st->empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.status)) {
-          ok = false;
-          break;
-        }
+        if (!mbar_wait(&st->empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.status)) break;
         mbar_arrive_expect_tx(&st->full[stage], bytes);
         tma_load_2d(stageA(stage), &tmA, &st->full[stage], kb * BK, m0);
         tma_load_2d(stageB0(stage), &tmB0, &st->full[stage], kb * BK, 0);
@@ -408,11 +404,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           phase ^= 1u;
         }
       }
-      if (!ok) {
-        int zero = 0;
-        for (long i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-          mbar_wait(&st->full[i % STAGES], (uint32_t)((i / STAGES) & 1), wind_down_ns(p.timeout_ns), &zero, p.status);
-      }
+      // wind down: let the copies already issued land before the CTA exits (also when a later warp's wait ran out)
+      int zero = 0;
+      for (long i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+        mbar_wait(&st->full[i % STAGES], (uint32_t)((i / STAGES) & 1), wind_down_ns(p.timeout_ns), &zero, p.status);
     }
   } else if (warp == 1) {
     if (lane == 0) {
