@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE, I8>::THREADS, 1)
         }
       }
       for (int kb = 0; kb < num_kb; ++kb) {
-        if (lane == 0) ok = mbar_wait(&st->empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.status);
+        if (lane == 0) ok = loader_wait<PAIR>(&st->empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.status);
         if (gathering) ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
         if (lane == 0 && leader) mbar_arrive_expect_tx(&st->full[stage], tx_bytes);
@@ -521,8 +521,9 @@ __global__ void __launch_bounds__(Cfg<PAIR, ST, WIDE, I8>::THREADS, 1)
         }
       }
     }
-    if (!PAIR && lane == 0) {
-      // wind down: let the copies already issued land before the CTA exits (also when a later warp's wait ran out)
+    if (leader && lane == 0) {
+      // wind down: let the copies already issued land before the CTA exits (also when a later warp's wait ran out); a
+      // pair's leader sees both CTAs', and the other CTA stays until the pair's last barrier
       int zero = 0;
       for (long i = issued > C::STAGES ? issued - C::STAGES : 0; i < issued; ++i)
         mbar_wait(&st->full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), wind_down_ns(p.timeout_ns), &zero, p.status);

@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                       (long long)((p.b_up_row + n0) / ATOM_ROWS) * atoms_k * ATOM_BYTES) /
                                      SF_ROW);
         for (int kb = 0; kb < num_kb; ++kb) {
-          ok = mbar_wait(&st->empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.status);
+          ok = loader_wait<PAIR>(&st->empty[stage], phase ^ 1u, p.timeout_ns, abort_flag, p.status);
           if (!ok) break;
           uint64_t* bar = &st->full[stage];
           if (PAIR) {
@@ -555,8 +555,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       }
-      if (!PAIR) {
-        // wind down: let the copies already issued land before the CTA exits (also when a later warp's wait ran out)
+      if (leader) {
+        // wind down: let the copies already issued land before the CTA exits (also when a later warp's wait ran out); a
+        // pair's leader sees both CTAs', and the other CTA stays until the pair's last barrier
         int zero = 0;
         for (long i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
           mbar_wait(&st->full[i % STAGES], (uint32_t)((i / STAGES) & 1), wind_down_ns(p.timeout_ns), &zero, p.status);

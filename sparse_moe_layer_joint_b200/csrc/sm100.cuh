@@ -91,6 +91,20 @@ __device__ __forceinline__ uint64_t wind_down_ns(uint64_t timeout_ns) {
   return timeout_ns > 1000000000ull ? timeout_ns : 1000000000ull;
 }
 
+// A loader's wait for a stage to be handed back.  In a pair both CTAs' copies complete on the leader's barriers, and the
+// stages are handed back to both at once: when neither loader stops before its own wait runs out, and none of them runs
+// out before the products have stopped, both have begun the same copies, and the leader can see them all land.  So a
+// pair's loaders take no notice of the other warps, and wait at least as long as for copies in flight.
+template <bool PAIR>
+__device__ __forceinline__ bool loader_wait(uint64_t* empty, uint32_t parity, uint64_t timeout_ns,
+                                            volatile int* abort_flag, unsigned int* status) {
+  if (!PAIR) return mbar_wait(empty, parity, timeout_ns, abort_flag, status);
+  int ran_out = 0;
+  if (mbar_wait(empty, parity, wind_down_ns(timeout_ns), &ran_out, status)) return true;
+  *abort_flag = 1;
+  return false;
+}
+
 // ----------------------------------------------------------------------------
 // TMA (tiled tensor copies global -> shared, completion on an mbarrier)
 // ----------------------------------------------------------------------------

@@ -11,7 +11,7 @@ if torch.cuda.is_available():
     from test_gpu_nvfp4 import _gemm_inputs
 
 
-def run_short(call, outputs):
+def run_short(call, outputs, times=10):
     """Calls with a limit of 1 ns; outputs() names what a whole call fills with one set of bits."""
     call()
     torch.cuda.synchronize()
@@ -20,7 +20,7 @@ def run_short(call, outputs):
     whole = lambda: all(torch.equal(a, b) for a, b in zip(want, outputs()))
     moe.moe_set_wait_timeout_ns(1)
     try:
-        for _ in range(10):
+        for _ in range(times):
             for t in outputs():
                 t.zero_()
             call()
@@ -49,8 +49,9 @@ def test_router(monkeypatch):
               lambda: (idx, gates, counts))
 
 
-def test_nvfp4_product(monkeypatch):
-    monkeypatch.setenv("MOE_FP4_PAIR", "0")
+@pytest.mark.parametrize("pair", ["0", "1"])
+def test_nvfp4_product(monkeypatch, pair):
+    monkeypatch.setenv("MOE_FP4_PAIR", pair)
     sizes, N, K = [130, 0, 64, 300], 512, 1024
     _, _, _, _, rows_cap, dev = _gemm_inputs(sizes, N, K, 3)
     n = sum(sizes)
@@ -58,7 +59,24 @@ def test_nvfp4_product(monkeypatch):
     out = torch.empty(n, N, dtype=torch.bfloat16, device="cuda")
     run_short(lambda: moe.moe_nvfp4_grouped_gemm(dev["aq"], dev["asf"], dev["off_pad"], 4, rows_cap, dev["wq"], dev["wsf"],
                                                  dev["g"], N, K, moe.MOE_NVFP4_EPI_BF16, None, None, out, off, n),
-              lambda: (out,))
+              lambda: (out,), 3 if pair == "1" else 10)  # a pair's loaders give up after a second
+
+
+@pytest.mark.parametrize("act", ["MOE_ACT_GELU_TANH", "MOE_ACT_SWIGLU"])
+@pytest.mark.parametrize("cta", ["1", "2"])
+def test_bf16_products(monkeypatch, cta, act):
+    monkeypatch.setenv("MOE_GEMM_CTA", cta)
+    counts, d, f = [130, 0, 64, 700], 1024, 512
+    n, f1 = sum(counts), 1024 if act == "MOE_ACT_SWIGLU" else 512
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(n, d, generator=g).bfloat16().cuda()
+    w1 = (torch.randn(4, f1, d, generator=g) / d ** 0.5).bfloat16().cuda()
+    w2 = (torch.randn(4, d, f, generator=g) / f ** 0.5).bfloat16().cuda()
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    h = torch.empty(n, f, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(n, d, dtype=torch.bfloat16, device="cuda")
+    run_short(lambda: moe.moe_grouped_ffn(x, off, 4, n, 0, w1, w2, d, f, getattr(moe, act), h, y), lambda: (h, y),
+              3 if cta == "2" else 10)
 
 
 def test_int8_product():
