@@ -447,7 +447,8 @@ int moe_int8_grouped_gemm(const int8_t* aq, const float* a_scale, const int32_t*
  * fp32 values) are coded as moe_int8_quantize_rows does.
  *   scratch    device buffer of at least moe_few_tokens_scratch_bytes(...) bytes,
  *              16-byte aligned, contents need not be initialised; calls that share
- *              one must be ordered
+ *              one must be ordered.  The size for T tokens is enough for any call
+ *              with fewer, of either precision and activation.
  * Results do not depend on timing: equal inputs give equal bits.
  * The launch is cooperative (one CTA per SM, all resident); its internal waits are
  * bounded by moe_set_wait_timeout_ns.

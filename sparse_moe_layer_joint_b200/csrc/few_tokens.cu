@@ -1181,12 +1181,13 @@ extern "C" size_t moe_few_tokens_scratch_bytes(int T, int d, int d_ff, int n_rou
   if (T <= 0 || T > MOE_FEW_MAX_T || d <= 0 || d > MOE_FEW_MAX_WIDTH || d_ff <= 0 || d_ff > MOE_FEW_MAX_WIDTH ||
       n_routed < 1 || n_shared < 0 || n_shared > MOE_MAX_SHARED || top_k < 1 || top_k > MOE_MAX_TOP_K)
     return 256;
-  // what any form of the call with these sizes needs
+  // what any form of the call with up to T tokens needs (fewer tokens may have more slices of K, and need more)
   size_t most = 0;
-  for (int form = 0; form < 4; ++form) {
-    const size_t b = few::layout_of(T, d, d_ff, n_routed, n_shared, top_k, (form & 1) != 0, 1 + (form >> 1)).bytes;
-    most = b > most ? b : most;
-  }
+  for (int t = 1; t <= T; ++t)
+    for (int form = 0; form < 4; ++form) {
+      const size_t b = few::layout_of(t, d, d_ff, n_routed, n_shared, top_k, (form & 1) != 0, 1 + (form >> 1)).bytes;
+      most = b > most ? b : most;
+    }
   return most;
 }
 

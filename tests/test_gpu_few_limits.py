@@ -34,3 +34,17 @@ def test_a_limit_that_no_barrier_keeps_is_reported(case, int8):
     assert set(seen) <= {0, moe.MOE_STATUS_TIMEOUT} and moe.MOE_STATUS_TIMEOUT in seen, seen
     c.out.fill_(float("nan"))
     c().check()
+
+
+@pytest.mark.parametrize("int8", [False, True], ids=["bf16", "int8"])
+def test_one_scratch_buffer_serves_every_smaller_call(int8):
+    """A buffer sized once for the most tokens, as a serving program has it; 6 tokens need more of it than 7."""
+    layer = (2048, 768, 64, 2, 4, "gelu")
+    d, f, n, ns, k, _ = layer
+    nb = moe.moe_few_tokens_scratch_bytes(64, d, f, n, ns, k)
+    scratch = torch.full((nb,), 0xff, dtype=torch.uint8, device="cuda")
+    for T in (7, 1, 6, 20, 3):
+        p = make(T, *layer, seed=T)
+        c = Call(to_int8(p) if int8 else p)
+        c.scratch, c.nb = scratch, nb
+        c().check()
