@@ -44,7 +44,8 @@
  *    out of range, inconsistent counts) set bits in a per-device status word
  *    that moe_get_status() reads and clears.
  *  - T = 0 (no tokens) is valid: the call does nothing except what it states
- *    (moe_router_topk still zeroes counts).
+ *    (moe_router_topk and moe_few_tokens* still zero counts).  The moe_int8_* and
+ *    moe_few_tokens* calls then take NULL for the tensors without elements.
  *  - Host-only calls (no stream, nothing launched): moe_permute_scratch_bytes,
  *    moe_nvfp4_rows_capacity, moe_few_tokens_scratch_bytes, moe_capacity_for,
  *    moe_status_string, moe_set_wait_timeout_ns and the moe_ipc_* mappings.

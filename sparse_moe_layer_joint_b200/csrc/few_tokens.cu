@@ -1079,8 +1079,8 @@ int run(const moe_bf16* x, const moe_bf16* w_router, const float* bias, const fl
         const float* w1s, const void* w2, const float* w2s, int T, int d, int d_ff, int n_routed, int n_shared,
         int top_k, float route_scale, int activation, int32_t* topk_idx, float* gates, int32_t* counts, moe_bf16* out,
         void* scratch, size_t scratch_bytes, void* stream) {
-  if (!x || !w_router || !bias || !w1 || !w2 || !topk_idx || !gates || !counts || !out || !scratch)
-    return MOE_ERR_INVALID_ARG;
+  if (!w_router || !bias || !w1 || !w2 || !counts || !scratch) return MOE_ERR_INVALID_ARG;
+  if (T != 0 && (!x || !topk_idx || !gates || !out)) return MOE_ERR_INVALID_ARG;  // without elements: perhaps no address
   if (I8 && (!w1s || !w2s)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(w1) || !aligned16(w2) || !aligned16(out) ||
       !aligned16(scratch) || !aligned4(bias) || !aligned4(logit_offset) || !aligned4(topk_idx) || !aligned4(gates) ||

@@ -154,9 +154,9 @@ using namespace moe;
 extern "C" int moe_int8_quantize_rows(const moe_bf16* x, long long rows, int K, int8_t* q, float* scale,
                                       void* stream) {
   if (rows < 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return K % 8 != 0 ? MOE_ERR_UNSUPPORTED : MOE_OK;  // tensors without elements may have no address
   if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned4(scale)) return MOE_ERR_INVALID_ARG;
   if (K % 8 != 0) return MOE_ERR_UNSUPPORTED;
-  if (rows == 0) return MOE_OK;
   q8::Params p{};
   p.x = reinterpret_cast<const uint4*>(x);
   p.rows = rows;
@@ -169,11 +169,11 @@ extern "C" int moe_int8_quantize_rows(const moe_bf16* x, long long rows, int K, 
 extern "C" int moe_int8_dispatch(const moe_bf16* x, const int32_t* token_row, int T, int d, int top_k, int n_rows,
                                  int8_t* xq, float* xs, int8_t* xq_tok, float* xs_tok, void* stream) {
   if (T < 0 || d <= 0 || top_k < 1 || top_k > MOE_MAX_TOP_K || n_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return d % 8 != 0 ? MOE_ERR_UNSUPPORTED : MOE_OK;  // tensors without elements may have no address
   if (!x || !token_row || !xq || !xs || !aligned16(x) || !aligned4(token_row) || !aligned16(xq) || !aligned4(xs) ||
       !aligned16(xq_tok) || !aligned4(xs_tok) || (xq_tok == nullptr) != (xs_tok == nullptr))
     return MOE_ERR_INVALID_ARG;
   if (d % 8 != 0) return MOE_ERR_UNSUPPORTED;
-  if (T == 0) return MOE_OK;
   q8::Params p{};
   p.x = reinterpret_cast<const uint4*>(x);
   p.rows = T;

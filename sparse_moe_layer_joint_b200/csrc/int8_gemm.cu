@@ -33,13 +33,14 @@ extern "C" int moe_int8_grouped_gemm(const int8_t* aq, const float* a_scale, con
   if (n_groups < 0 || n_rows < 0 || expert_base < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
   if (epilogue != MOE_INT8_EPI_BF16 && epilogue != MOE_INT8_EPI_GELU && epilogue != MOE_INT8_EPI_SWIGLU)
     return MOE_ERR_INVALID_ARG;
-  if (!aq || !a_scale || !wq || !w_scale || !out) return MOE_ERR_INVALID_ARG;
+  const bool empty = n_rows == 0 || n_groups == 0;  // tensors without elements may have no address
+  if (!empty && (!aq || !a_scale || !wq || !w_scale || !out)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(aq) || !aligned4(a_scale) || !aligned4(offsets) || !aligned16(wq) || !aligned16(w_scale) ||
       !aligned16(out))
     return MOE_ERR_INVALID_ARG;
   if (K % 16 != 0 || K > 131072 || N % 32 != 0 || N > 0x3fffffff || n_groups > MOE_MAX_GROUPS)
     return MOE_ERR_UNSUPPORTED;
-  if (n_rows == 0 || n_groups == 0) return MOE_OK;
+  if (empty) return MOE_OK;
   const bool identity = offsets == nullptr;
   const long long out_rows = identity ? (long long)n_groups * n_rows : n_rows;
   if (out_rows > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
