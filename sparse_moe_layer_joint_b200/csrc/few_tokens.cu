@@ -1021,13 +1021,17 @@ struct Layout {
 };
 
 // log2 of the K slices of a matrix of nch chunks, for `units` blocks of 16 rows.  A phase ends when the last warp's last
-// item does, so an item should be short beside the phase: at least one and a half items for each of 2368 warps, and as
-// long as they are fewer than sixteen each, at most 8 chunks of K (about 12 us).  Every item costs a ticket, its places and its partial sums,
-// so it keeps at least two chunks.  (32 tokens, SwiGLU, d 4096: items of 32 chunks left the first SM idle for 34 us.)
+// item does, so an item should be short beside the phase: at least one and a half items for each warp, and as long as they
+// are fewer than sixteen each, at most 8 chunks of K (about 12 us).  Every item costs a ticket, its places and its partial
+// sums, so it keeps at least two chunks.  (32 tokens, SwiGLU, d 4096: items of 32 chunks left the first SM idle for 34 us.)
+// The warps are those of 148 SMs whatever the device has: the scratch's size goes by the slices and is computed without a
+// device, and on another SM count only the balance is off.
+constexpr double NOMINAL_WARPS = 148.0 * WARPS;
+
 inline int slices_log(double units, int nch) {
   int s = 0;
   while ((1 << (s + 1)) <= S_MAX && (nch >> (s + 1)) >= 2 &&
-         (units * (1 << s) < 1.5 * 2368 || ((nch >> s) > 8 && units * (1 << s) < 16.0 * 2368)))
+         (units * (1 << s) < 1.5 * NOMINAL_WARPS || ((nch >> s) > 8 && units * (1 << s) < 16.0 * NOMINAL_WARPS)))
     ++s;
   return s;
 }
