@@ -445,14 +445,19 @@ int moe_int8_grouped_gemm(const int8_t* aq, const float* a_scale, const int32_t*
  * 8-bit experts: w1 [n, d_ff, d] (SwiGLU [n, 2*d_ff, d]) and w2 [n, d, d_ff] int8
  * with scales w1_scale [n, d_ff or 2*d_ff] and w2_scale [n, d] from
  * moe_int8_quantize_rows, n = n_routed + n_shared; x rows and hidden rows (the
- * fp32 values) are coded as moe_int8_quantize_rows does.
+ * fp32 values) are coded as moe_int8_quantize_rows does, except that an fp32 value
+ * whose 127 v / a lies below a half-integer by less than 2^-23 of itself may get the
+ * next code.
  *   scratch    device buffer of at least moe_few_tokens_scratch_bytes(...) bytes,
  *              16-byte aligned, contents need not be initialised; calls that share
  *              one must be ordered.  The size for T tokens is enough for any call
  *              with fewer, of either precision and activation.
  * Results do not depend on timing: equal inputs give equal bits.
  * The launch is cooperative (one CTA per SM, all resident); its internal waits are
- * bounded by moe_set_wait_timeout_ns.
+ * bounded by moe_set_wait_timeout_ns (there: what is waited for longer).  After a wait
+ * that ran out the outputs are undefined; the next call needs nothing cleared.
+ * An infinite weight may give NaN where the exact result is infinite (bf16 experts:
+ * the hidden rows' two parts are multiplied separately).
  * Limits: T <= MOE_FEW_MAX_T, d % 64 == 0, d_ff % 64 == 0, d and d_ff <=
  * MOE_FEW_MAX_WIDTH, n_routed <= 256, n_shared <= 8, top_k <= 8.
  * MOE_ERR_SCRATCH when scratch_bytes is too small.
@@ -586,7 +591,11 @@ int moe_get_status(void* stream, int* device_status);
 /*
  * moe_set_wait_timeout_ns -- limit, in nanoseconds, on every device-side wait
  * of the kernels launched afterwards (default 2e9).  A wait that runs out sets
- * MOE_STATUS_TIMEOUT and its kernel winds down and returns.
+ * MOE_STATUS_TIMEOUT and its kernel winds down and returns.  Winding down, a
+ * kernel waits for its own copies and products in flight, and the loaders of a
+ * pair of CTAs for stages that are not handed back, for up to the larger of the
+ * limit and one second each: shared memory and tensor memory are not given back
+ * before.
  */
 int moe_set_wait_timeout_ns(uint64_t ns);
 

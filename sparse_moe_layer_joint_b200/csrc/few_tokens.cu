@@ -42,10 +42,11 @@
 // The grid barriers need every CTA resident: the launch is cooperative, and every
 // wait is bounded (wait_timeout_ns, MOE_STATUS_TIMEOUT).
 //
-// Measured (256 + 2 experts, top-6, GELU, d 7168, d_ff 2048; the HBM floor at 6.53
-// TB/s in brackets): one token 92 us in bf16 (72) and 55 in 8 bits (37), 8 tokens
-// 423 and 225, 64 tokens 1940 and 1010; in separate launches (router, dispatch,
-// grouped GEMMs, combine) 210 and 175, 508 and 360, 2114 and 1090.  The weights
+// Measured (256 + 2 experts, top-6, GELU, d 7168, d_ff 2048, CUDA graphs of 8 batches;
+// the HBM floor at 6.53 TB/s in brackets): one token 92 us in bf16 (72) and 55 in 8
+// bits (37), 8 tokens 425 and 225, 64 tokens 1830 to 1940 and 910 to 1010; in separate
+// launches (router, dispatch, grouped GEMMs, combine) 206 and 173, 512 and 354, 2120
+// and 1080.  The weights
 // stream at 6.1 to 7 TB/s; what remains beside them, 18 us at one token, is the
 // launch, the router and its barrier (9), the two barriers around the hidden rows
 // (8) and the last sums (5), less what the rings load meanwhile.  A layer of d 256
@@ -907,7 +908,9 @@ __device__ __forceinline__ bool route_all(const Params& p, Smem* sm) {
 }
 
 // NTM: tiles of 8 tokens an expert can have, 1, 2 or 8 by the call's T.  (The code for more than two needs more registers
-// than there are; with it one token at d 7168, d_ff 2048 took 94 us instead of 91.)
+// than there are; with it one token at d 7168, d_ff 2048 took 94 us instead of 91.  It spills 344 bytes a thread in bf16
+// and 384 in 8 bits, which narrow layers feel: d 1024, d_ff 512, 64 + 2 experts take 47 and 39 us with 16 tokens, 57 and 43
+// with 17.)
 template <bool I8, int NTM>
 __global__ void __launch_bounds__(THREADS, 1)
     few_tokens_kernel(const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,

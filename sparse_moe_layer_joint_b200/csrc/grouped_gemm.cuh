@@ -270,8 +270,8 @@ __device__ __forceinline__ void apply_scales(float (&v)[N], float row_scale, con
 
 // Epilogue warps of the 8-bit kernel.  A warp drains 32 rows by half of the tile's columns, 32 outputs of every row at a
 // time: scales and activation in registers, then through shared memory, so that a store writes whole 64-byte pieces of
-// eight rows (a lane's own row in 16-byte stores left half of each 32-byte sector to another store: 8192 tokens of
-// d_ff 768 -> d 2048 took 104 us).  The channel scales are fetched while the tile's products run.
+// eight rows (a lane's own row in 16-byte stores left half of each 32-byte sector to another store: 4095 tokens of
+// d_ff 768 -> d 2048 took 141 us instead of 104).  The channel scales are fetched while the tile's products run.
 template <int EPI, class TailT>
 __device__ __forceinline__ void epilogue_i8(const Params& p, TailT* st, uint32_t tmem_base, int unit, int n_units,
                                             int total_tiles, int G, int warp, int lane) {
@@ -945,9 +945,7 @@ int run_gemm(const GemmSpec& g, bool pair, int stages, int sms, long long tiles_
   if ((rc = encode(&b, g.b, 3, K, N, (uint64_t)(g.p.G_r + g.p.G_s), KE, b_box)) != MOE_OK) return rc;
   long long units = tiles_upper * p.n_tiles_n;
   if constexpr (I8) {
-    // single CTAs at every size: 128 x 256 tiles with two accumulators beat pair tiles, whose products end sooner but
-    // whose one accumulator makes them wait for the epilogue (1536 rows a group, K 7168, N 2048: 537 us against 589 on
-    // 256 x 512 pair tiles and 551 on 256 x 256; only a single group of 9472 rows with K 16384 ran 12% faster on pairs)
+    // single CTAs at every size (int8_gemm.cu has the measurements)
     return launch_one<EPI, false, 4, false, true>(a0, a1, b, p, (int)(units < sms ? units : sms), s);
   } else {
     if (pair) {

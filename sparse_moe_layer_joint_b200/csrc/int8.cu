@@ -7,9 +7,10 @@
 // vectors a thread, TPR threads a row), so it is read once; rows of more than
 // 16384 values are read a second time, from L2.  A value costs one conversion, one
 // fma and three quarters of a byte permute (int8.cuh): 24570 rows of 2048 take 25.8
-// us (5.9 TB/s), the dispatch of 16384 tokens of 4096 to six experts 94 us (6.4
-// TB/s), one 2048 x 7168 matrix 12 us (7.9 when it lies in L2), the
-// dispatch of 64 tokens of 7168 3.1 us.
+// us in the kernel alone (5.9 TB/s; 28 a call when calls follow each other), the
+// dispatch of 16384 tokens of 4096 to six experts 94 (6.4 TB/s; 98), one 2048 x 7168
+// matrix 12 (7.9 when it lies in L2; its 1024 blocks are 1.4 waves of the 740 that 96
+// registers a thread allow), the dispatch of 64 tokens of 7168 3.1 (8).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

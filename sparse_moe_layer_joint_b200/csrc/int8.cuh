@@ -1,5 +1,5 @@
 // int8.cuh -- symmetric 8-bit codes of a row: with a = max |v| over the row,
-//   scale = fl32(a / 127),  code = round-half-even(127 v / a),
+//   scale = fl32(a / 127),  code = round-half-even(127 v / a)  (exact for bf16 values, see to_code for fp32),
 // a row of zeros has scale 0 and codes 0, and a row that holds a NaN or an
 // infinity has scale NaN and codes 0 (whatever it is multiplied with is NaN).
 #pragma once
@@ -45,6 +45,8 @@ __device__ __forceinline__ uint32_t abs_max_bits(const uint4& v) {
 // inv and the product are exact.  If it divides o <= 253, then o = 127, |v| = a / 2, and inv rounded up makes the product
 // 63.5 or just above: 64, the even neighbour, either way.  Every other quotient is at least 1.5e-5 of its value away
 // from a half-integer, and inv is within 1.2e-7 of 127 / a.
+// For fp32 values (the few-token layer's hidden rows) a quotient that lies below a half-integer by less than 2^-23 of itself
+// may go to the code above; every other one is exact.
 __device__ __forceinline__ uint32_t to_code(float v, float inv) { return __float_as_uint(__fmaf_rn(v, inv, 12582912.0f)); }
 
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {

@@ -3,20 +3,26 @@
 // grouped_gemm.cuh on kind::i8 tensor cores.  The int32 sums are exact, so a
 // result is one product of the two scales and the sum, whatever the tiling.
 //
-// Why single CTAs of 128 x 256 (a pair's 256 x 256 tile reads a third less into each
-// SM): experts rarely have whole 256-row tiles, and 128-row tiles leave less of them
-// empty; pairs were 6-8% faster with 129 to 256 rows a group and slower or equal
-// elsewhere.  Eight epilogue warps drain one accumulator while the other fills, and
-// send their outputs through shared memory so that every store is whole sectors.
+// Why single CTAs of 128 x 256, although a pair's 256 x 256 tile reads a third less into
+// each SM: 128-row tiles leave less of a group's last tile empty, and where they do not
+// the power limit, not the reads, sets the pace of calls that follow each other.  Even
+// groups, calls back to back, pairs with four and with five stages against single CTAs:
+// 144 to 256 rows a group (K 7168, N 2048, GELU) 6 to 9% slower with four, 1% faster to
+// 4% slower with five (224 rows: 1112 and 1043 against 1051 us); 512 rows 4 and 1%
+// slower; 1536 rows 11 and 9%; 64 to 128 and 320 to 384 rows, whose last 256-row tile is
+// half empty, 33 to 70%; random or skewed sizes of 192 to 512 rows on average 5 to 41%.
+// (The fastest of eight rounds, before the limit sets in, was up to 8% faster on pairs.)
+// Eight epilogue warps drain one accumulator while the other fills, and send their
+// outputs through shared memory so that every store is whole sectors.
 //
 // What bounds it.  Many rows: 8-bit products take half the tensor time of bf16 at the
 // same bytes a row of K, so a 128 x 256 tile asks L2 for 96 bytes a clock, more than
 // the 64 or so that an SM gets, and under a sustained load the power limit lowers the
 // clock.  256 groups of 192 rows, K 7168, N 2048, GELU: 219 us a quarter of it alone
-// (1.65 POP/s; the weights and rows take 163 at 6.53 TB/s), 1000 to 1100 us for all of
-// it repeated for seconds.  32 groups of 1536 rows: 640 us (2.25 POP/s).  Few rows: the
-// weights.  256 groups of 1.5 rows, K 4096, 2 x 1024 channels (SwiGLU): 279 us, 6.0
-// TB/s.
+// (1.65 POP/s; the weights and rows take 163 at 6.53 TB/s), 990 to 1120 us for all of
+// it back to back (by GPU).  32 groups of 1536 rows: 585 to 640 us (2.25 to 2.47
+// POP/s).  Few rows: the weights.  256 groups of 1.5 rows, K 4096, 2 x 1024 channels
+// (SwiGLU): 279 to 300 us, 5.6 to 6.0 TB/s.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

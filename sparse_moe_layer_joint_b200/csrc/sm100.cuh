@@ -365,8 +365,10 @@ __device__ __forceinline__ float gelu_tanh_f32(float u) {
   return 0.5f * u * (1.0f + tanh_approx(inner));
 }
 
-// The same function through u (1 + tanh a) / 2 = u / (1 + e^-2a), within a few fp32 rounding steps (the
-// hardware tanh is off by up to 2^-11): for results that are kept in more than bf16 or coded to 8 bits.
+// The same function through u (1 + tanh b) / 2 = u / (1 + e^-a) with a = 2b, for results that are kept in more than bf16
+// or coded to 8 bits (the hardware tanh is off by up to 2^-11).  The error of a's own roundings and of the exponential
+// grows with |a|: the result is within (8 |a| + 16) 2^-24 of itself, a few rounding steps where u is small or positive
+// and some hundred in the far negative tail, where the value is next to nothing.
 __device__ __forceinline__ float gelu_tanh_exp_f32(float u) {
   const float k0 = 0.7978845608028654f;  // sqrt(2/pi)
   const float k1 = 0.044715f;
