@@ -11,7 +11,7 @@
 // 4% slower with five (224 rows: 1112 and 1043 against 1051 us); 512 rows 4 and 1%
 // slower; 1536 rows 11 and 9%; 64 to 128 and 320 to 384 rows, whose last 256-row tile is
 // half empty, 33 to 70%; random or skewed sizes of 192 to 512 rows on average 5 to 41%.
-// (The fastest of eight rounds, before the limit sets in, was up to 8% faster on pairs.)
+// (The fastest of eight repetitions, before the limit sets in, was up to 8% faster on pairs.)
 // Eight epilogue warps drain one accumulator while the other fills, and send their
 // outputs through shared memory so that every store is whole sectors.
 //
