@@ -248,7 +248,7 @@ struct StreamEnv {
   __device__ __forceinline__ void queue(int at, int item) { sm->queue[threadIdx.x >> 5][at] = item; }
   __device__ __forceinline__ int expert(int j) const { return expert_at(p, sm, j); }
   __device__ __forceinline__ unsigned int draw() { return atomicAdd(p.bar + 4, 1u); }
-  // (a ring wait's flag is seen by every lane 0: a block barrier lies between the items and the next fill)
+  // (a ring wait's flag is seen by every lane 0: a block barrier lies between phase 1's items and phase 2's first loads)
   __device__ __forceinline__ bool ran_out() const { return sm->abort_flag != 0; }
   __device__ __forceinline__ unsigned int warps() const { return gridDim.x * WARPS; }
 
